@@ -119,7 +119,12 @@ enum {
   GQE_WS_ATTENTION = 4, /* scratch of gqe_attention_fwd (split-KV partials) */
   GQE_WS_DECODE = 5,    /* scratch of gqe_decode_step */
   GQE_WS_DENSE_DECODE = 6, /* scratch of gqa_dense_decode_step */
-  GQE_WS_BACKWARD = 7      /* scratch of gqe_layer_bwd */
+  GQE_WS_BACKWARD = 7,     /* scratch of gqe_layer_bwd */
+  GQE_WS_QK_ROPE = 8,      /* scratch of gqe_qk_rope_bwd */
+  GQE_WS_BALANCE = 9,      /* scratch of gqe_balance_stats */
+  GQE_WS_KV4 = 10,         /* scratch of gqe_kv4_attention */
+  GQE_WS_DECODE_KV4 = 11,  /* scratch of gqe_decode_step_kv4 */
+  GQE_WS_BACKWARD_AUX = 12 /* scratch of gqe_layer_bwd_aux */
 };
 
 /* Items inside the GQE_WS_LAYER / GQE_WS_DENSE workspaces (for inspection). */
@@ -395,6 +400,206 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
                          const gqe_bf16* W_o, const float* dy, float* dx, float* dW_r, float* db_r,
                          float* dW_q, float* dW_qs, float* dW_k, float* dW_v, float* dW_o, void* ws,
                          size_t ws_bytes, gqe_stream_t stream);
+
+/*
+ * Query/key norm and position rotation, for layers that need positions (the
+ * pages' layer has none: these are additions of this library, placed between
+ * the projections and the attention). For every row x (the d_head values of
+ * one head at one token):
+ *   n = w * x * rsqrt(mean(x^2) + eps)   with GQE_ROPE_NORM; else n = x
+ *   pair i < d_rot/2 of n, (a, b) = (n[i], n[i + d_rot/2]), or with
+ *   GQE_ROPE_ADJACENT (n[2i], n[2i+1]):
+ *     angle = pos[axis[i]][row] * inv_freq[i]
+ *     (a, b) <- scale * (a cos - b sin, a sin + b cos)
+ *   elements d_rot and up pass.
+ * Angles are formed in fp64, the rest in fp32, one rounding at the end.
+ */
+#define GQE_ROPE_NORM 1u     /* norm each row over d_head first */
+#define GQE_ROPE_ADJACENT 2u /* pairs of adjacent elements */
+
+typedef struct gqe_rope {
+  int32_t d_rot;          /* rotated elements: a multiple of 8, 0..d_head */
+  int32_t axes;           /* axes of a position, 1..4 (time, height, ...) */
+  uint32_t flags;         /* GQE_ROPE_* */
+  float eps;              /* of the norm */
+  float scale;            /* factor of the rotated pairs (1: a plain rotation) */
+  const int32_t* pos;     /* [axes, B*T]; NULL: the token's index t on every axis */
+  const double* inv_freq; /* [d_rot/2], radians per position (NULL if d_rot = 0) */
+  const int32_t* axis;    /* [d_rot/2], each in [0, axes); NULL: axis 0. An
+                           * entry outside is taken as 0 and recorded in the
+                           * status word (GQE_ERR_DEVICE_CHECK) */
+  const float* w_q;       /* [d_head] norm weights of the queries (routed and
+                           * shared); NULL: ones */
+  const float* w_k;       /* [d_head] norm weights of the keys; NULL: ones */
+} gqe_rope;
+
+/*
+ * Applies `rope` to the routed queries Q, the shared head's Qs and the keys K
+ * in one launch. Any of the three may be NULL with its output (left out);
+ * each output may be its input. Dense heads: cfg->k = M (Q [B, G*M, T, d_head]).
+ * Q, Qo [B, G, k, T, d_head], or with slot_pos (from gqe_dispatch) in
+ * token-list order [k*G*B*T, d_head]; slot_pos [B*T, G, k] or NULL (an entry
+ * outside the list: the row is skipped and GQE_ERR_DEVICE_CHECK recorded).
+ * Qs, Qso [B, T, d_head]; K, Ko [B, G, T, d_head].
+ */
+gqe_status gqe_qk_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* Q, const gqe_bf16* Qs,
+                       const gqe_bf16* K, const int32_t* slot_pos, gqe_bf16* Qo, gqe_bf16* Qso, gqe_bf16* Ko,
+                       gqe_stream_t stream);
+
+/*
+ * Backward of gqe_qk_rope: gradients (fp32) of its inputs and norm weights
+ * from those of its outputs. Q, Qs, K: the forward's inputs (the operands of
+ * the gradients that are NULL are not read); without GQE_ROPE_NORM they are
+ * not read and may be NULL. dQ, dQs, dK in the layout of Q, Qs, K, each may
+ * be its dQo, dQso, dKo. dw_q, dw_k [d_head] (overwritten; summed over every
+ * row in a fixed order), or NULL: not computed; with GQE_ROPE_NORM only.
+ * ws >= gqe_workspace_bytes(cfg, GQE_WS_QK_ROPE) bytes.
+ */
+gqe_status gqe_qk_rope_bwd(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* Q, const gqe_bf16* Qs,
+                           const gqe_bf16* K, const int32_t* slot_pos, const float* dQo, const float* dQso,
+                           const float* dKo, float* dQ, float* dQs, float* dK, float* dw_q, float* dw_k, void* ws,
+                           size_t ws_bytes, gqe_stream_t stream);
+
+/*
+ * The router's logits alone: z[row, e] = x[row] . W_r[:, e] + b_r[e], fp32
+ * (one fp32 sum; the certified selection is gqe_router_topk's). z [B*T, N].
+ */
+gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r, float* z,
+                             gqe_stream_t stream);
+
+/*
+ * Balance loss of the router, in two steps. The pages say that a
+ * load-balancing loss is used and give no formula; this is the usual product
+ * of load and mean probability, per group. With p the softmax of a group's M
+ * logits, n the counted rows, c[e] the counted rows that selected expert e:
+ *   L_balance = (M/G) sum_e (c[e] / (k n)) * (1/n) sum_rows p[row, e]
+ *   L_z       = 1/(n G) sum_{rows, g} (log sum_j exp z[row, g, j])^2
+ *   loss      = c_balance * L_balance + c_z * L_z
+ *   dz[row, g, j] = c_balance M/(G n) p_j (f_j - sum_i p_i f_i)
+ *                   + c_z 2/(n G) lse p_j,    f = c / (k n), counts fixed.
+ *
+ * gqe_balance_stats: counts [N+1] int32 (per expert; then n) and sums [N+1]
+ * fp32 (sum of p per expert; then the sum of lse^2). Ranks that share a batch
+ * add theirs up before the second step.
+ * gqe_balance_loss: loss [3] fp32 (loss, L_balance, L_z) or NULL, and dz
+ * [B*T, N] fp32 or NULL; `accumulate` adds to dz instead of writing it.
+ *
+ * z [B*T, N] fp32; idx [B*T, G, k] int32 (gqe_router_topk; an entry outside
+ * 0..M-1 counts for no expert); mask [B*T] bytes, 0 = not counted (its logits
+ * are not looked at, its dz is 0), or NULL. No row counted: loss and dz 0.
+ * ws >= gqe_workspace_bytes(cfg, GQE_WS_BALANCE) bytes.
+ */
+gqe_status gqe_balance_stats(const gqe_config* cfg, const float* z, const int32_t* idx, const uint8_t* mask,
+                             int32_t* counts, float* sums, void* ws, size_t ws_bytes, gqe_stream_t stream);
+gqe_status gqe_balance_loss(const gqe_config* cfg, const float* z, const uint8_t* mask, const int32_t* counts,
+                            const float* sums, float c_balance, float c_z, float* loss, float* dz, int accumulate,
+                            gqe_stream_t stream);
+
+/*
+ * K/V cache in 4 bits. A row (d_head values of one key or value) is d_head
+ * codes of 4 bits (byte i: element 2i in the low half, 2i+1 in the high half)
+ * and a bf16 (scale, zero) pair, value = zero + scale * code:
+ *   zero = min(row), scale = bf16((max(row) - min(row)) / 15),
+ *   code = clamp(round_half_even((x - zero) / scale), 0, 15), 0 if scale = 0;
+ * a row with an infinity or NaN is stored as all NaN.
+ */
+typedef struct gqe_kv4 {
+  uint8_t* k_codes; /* [B, G, capacity, d_head/2] */
+  uint8_t* v_codes;
+  gqe_bf16* meta;   /* [B, G, capacity, 4]: K scale, K zero, V scale, V zero */
+  int32_t capacity; /* keys per (sequence, group), a multiple of 16 */
+} gqe_kv4;
+
+/*
+ * gqe_kv4_append stores K, V [B, G, T, d_head] at positions start[b] + t of
+ * sequence b, for t < count[b]; gqe_kv4_read writes those positions back as
+ * bf16 (the other rows of K, V are left as they are), e.g. for a prefill that
+ * attends to a cached prefix. start [B] int32 or NULL (0), count [B] int32 or
+ * NULL (T). Positions before 0 are skipped; positions from capacity on are
+ * skipped and recorded (GQE_ERR_DEVICE_CHECK).
+ */
+gqe_status gqe_kv4_append(const gqe_config* cfg, const gqe_bf16* K, const gqe_bf16* V, const int32_t* start,
+                          const int32_t* count, const gqe_kv4* cache, gqe_stream_t stream);
+gqe_status gqe_kv4_read(const gqe_config* cfg, const gqe_kv4* cache, const int32_t* start, const int32_t* count,
+                        gqe_bf16* K, gqe_bf16* V, gqe_stream_t stream);
+
+/*
+ * Attention of one token per sequence over its 4-bit cache:
+ *   out = sum_u softmax_u(q . K[u] / sqrt(d_head)) V[u], u < lens[b]
+ * for the k routed heads of every group and, with Qs, the shared head (group
+ * 0). lens [B] int32, clamped to 0..cfg->T (NULL: cfg->T <= capacity; cfg->T
+ * sizes the launch, so a bound near the longest sequence is best). A sequence
+ * without keys gets zeros.
+ * Q [B, G, k, d_head] (dense heads: cfg->k = M); Qs [B, d_head] or NULL;
+ * out [B, ldo], ldo a multiple of 8: head (g, s) at column (g*k + s)*d_head,
+ * the shared head at k*G*d_head. At most 16 heads per group, B*G <= 65535.
+ * ws >= gqe_workspace_bytes(cfg, GQE_WS_KV4) bytes; calls sharing one ws must
+ * not overlap on the GPU.
+ */
+gqe_status gqe_kv4_attention(const gqe_config* cfg, const gqe_bf16* Q, const gqe_bf16* Qs, const gqe_kv4* cache,
+                             const int32_t* lens, gqe_bf16* out, int32_t ldo, void* ws, size_t ws_bytes,
+                             gqe_stream_t stream);
+
+/*
+ * gqe_layer_fwd with `rope` applied to Q, Qs and K before the attention (in
+ * place in the workspace). Arguments otherwise as in gqe_layer_fwd.
+ */
+gqe_status gqe_layer_fwd_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                              const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                              const gqe_bf16* W_v, const gqe_bf16* W_o, gqe_bf16* y, void* ws, size_t ws_bytes,
+                              gqe_stream_t stream);
+
+/* The balance loss of gqe_layer_bwd_aux: as in gqe_balance_stats and
+ * gqe_balance_loss; counts [N+1], sums [N+1] and loss [3] are outputs. */
+typedef struct gqe_balance {
+  const uint8_t* mask;
+  float c_balance, c_z;
+  int32_t* counts;
+  float* sums;
+  float* loss; /* or NULL */
+} gqe_balance;
+
+/*
+ * gqe_layer_bwd with the positions of gqe_layer_fwd_rope (rope NULL: none; its
+ * norm weights' gradients go to dw_qn, dw_kn [d_head], NULL: not computed) and
+ * with the gradient of the balance loss on the layer's own routing (balance
+ * NULL: none) added to that of the output: dx, dW_r, db_r then belong to the
+ * sum of both. Scratch: >= gqe_workspace_bytes(cfg, GQE_WS_BACKWARD_AUX).
+ */
+gqe_status gqe_layer_bwd_aux(const gqe_config* cfg, const gqe_rope* rope, const gqe_balance* balance,
+                             const gqe_bf16* x, const float* W_r, const float* b_r, const gqe_bf16* W_q,
+                             const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v, const gqe_bf16* W_o,
+                             const float* dy, float* dx, float* dW_r, float* db_r, float* dW_q, float* dW_qs,
+                             float* dW_k, float* dW_v, float* dW_o, float* dw_qn, float* dw_kn, void* ws,
+                             size_t ws_bytes, gqe_stream_t stream);
+
+/*
+ * gqe_decode_step with `rope` applied to the new token's queries and key
+ * (rope->pos [axes, B]; NULL: T - 1). The cache then holds rotated keys, as a
+ * prefill with the same rope writes them.
+ */
+gqe_status gqe_decode_step_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                                const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                                const gqe_bf16* W_v, const gqe_bf16* W_o, gqe_bf16* K_cache, gqe_bf16* V_cache,
+                                int32_t cache_capacity, gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream);
+
+/*
+ * Decode step over the 4-bit cache, sequences of their own lengths: the new
+ * token of sequence b is at position lens[b] (its cache holds 0..lens[b]-1),
+ * is stored there and attends to lens[b] + 1 keys. lens[b] = -1: an idle
+ * sequence of a padded batch (nothing stored, y[b] = 0). lens is not changed.
+ * A lens[b] of cfg->T or more is a caller's error: nothing is stored from
+ * capacity on (recorded, GQE_ERR_DEVICE_CHECK), at most cfg->T keys are read.
+ *   cfg->T   the most keys any sequence has after the step, <= capacity;
+ *   rope     or NULL; rope->pos [axes, B] (NULL: lens[b]);
+ *   lens     [B] int32 (NULL: T - 1 for every sequence).
+ * Weights and y as in gqe_decode_step.
+ * Scratch: >= gqe_workspace_bytes(cfg, GQE_WS_DECODE_KV4).
+ */
+gqe_status gqe_decode_step_kv4(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                               const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                               const gqe_bf16* W_v, const gqe_bf16* W_o, const gqe_kv4* cache, const int32_t* lens,
+                               gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream);
 
 #ifdef __cplusplus
 }

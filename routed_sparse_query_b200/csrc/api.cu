@@ -24,7 +24,8 @@ bool all_aligned(const P*... ps) {
   return ok;
 }
 
-gqe_status check_cfg(const gqe_config* c) {
+// What every call asks of a configuration.
+gqe_status check_shape(const gqe_config* c) {
   if (c == nullptr) return GQE_ERR_INVALID;
   if (c->B < 1 || c->T < 1 || c->G < 1 || c->M < 1 || c->k < 1 || c->k > c->M) return GQE_ERR_INVALID;
   if (c->d_model < 64 || c->d_model % 64 != 0 ||
@@ -37,6 +38,20 @@ gqe_status check_cfg(const gqe_config* c) {
     return GQE_ERR_INVALID;
   if (c->G * c->M > kMaxExperts || c->G > 32) return GQE_ERR_UNSUPPORTED;
   if (c->d_head != 32 && c->d_head != 64) return GQE_ERR_UNSUPPORTED;
+  return GQE_OK;
+}
+
+// The row operators (norm and rotation, balance loss, 4-bit cache): rows are
+// counted in int32, offsets in 64 bits.
+gqe_status check_rows(const gqe_config* c) {
+  const gqe_status s = check_shape(c);
+  if (s != GQE_OK) return s;
+  return static_cast<long long>(c->B) * c->T * c->G * c->k >= (1ll << 31) ? GQE_ERR_UNSUPPORTED : GQE_OK;
+}
+
+gqe_status check_cfg(const gqe_config* c) {
+  const gqe_status s = check_shape(c);
+  if (s != GQE_OK) return s;
   // Index arithmetic of the kernels stays within int32 for these extents.
   const long long R = static_cast<long long>(c->B) * c->T;
   const long long N = static_cast<long long>(c->G) * c->M;
@@ -202,6 +217,109 @@ DenseWs dense_ws(const gqe_config& c) {
   return L;
 }
 
+// Backward with positions and balance loss: the plain backward's workspace,
+// then the rotated Q, Qs, K (the workspace's own hold what the norm read) and
+// the scratch of the added operators.
+struct BwdAuxWs {
+  BwdWs W;
+  size_t Qv, Qs, K, scratch, total;
+};
+
+BwdAuxWs bwd_aux_ws(const gqe_config& c) {
+  BwdAuxWs A{};
+  A.W = bwd_ws(c);
+  const size_t R = static_cast<size_t>(c.B) * c.T, dh = c.d_head;
+  size_t o = round256(A.W.total);
+  auto put = [&](size_t& field, size_t bytes) {
+    field = o;
+    o = round256(o + bytes);
+  };
+  put(A.Qv, R * c.G * c.k * dh * 2);
+  put(A.Qs, R * dh * 2);
+  put(A.K, R * c.G * dh * 2);
+  const size_t rb = rope_bwd_ws_bytes(c.d_head), bb = balance_ws_bytes(c.G * c.M);
+  put(A.scratch, rb > bb ? rb : bb);
+  A.total = o;
+  return A;
+}
+
+struct DecodeKv4Ws {
+  LayerWs L1;
+  size_t aws, total;
+};
+
+DecodeKv4Ws decode_kv4_ws(const gqe_config& c) {
+  DecodeKv4Ws D{};
+  D.L1 = layer_ws(decode_rows_cfg(c));
+  D.aws = round256(D.L1.total);
+  D.total = D.aws + kv4_attention_ws_bytes(c.B, c.G, c.T, c.k + 1, c.d_head);
+  return D;
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+gqe_status check_rope(const gqe_config& c, const gqe_rope* r) {
+  if (r == nullptr || r->d_rot < 0 || r->d_rot > c.d_head || r->axes < 1 || r->axes > 4 ||
+      (r->flags & ~(GQE_ROPE_NORM | GQE_ROPE_ADJACENT)) != 0u || !(r->eps >= 0.0f) || (r->d_rot > 0 && r->inv_freq == nullptr))
+    return GQE_ERR_INVALID;
+  if (!aligned_to(r->inv_freq, 8) || !aligned_to(r->pos, 4) || !aligned_to(r->axis, 4) || !aligned_to(r->w_q, 4) ||
+      !aligned_to(r->w_k, 4))
+    return GQE_ERR_INVALID;
+  return r->d_rot % 8 != 0 ? GQE_ERR_UNSUPPORTED : GQE_OK;
+}
+
+RopeRows rope_rows(const void* p, long long sb, long long sh, long long st) {
+  return RopeRows{const_cast<void*>(p), sb, sh, st};  // inputs and outputs share the type
+}
+
+// The operator on the layer's layouts Q [B, G*k, T, dh], Qs [B, T, dh],
+// K [B, G, T, dh]; outputs of the same layouts.
+RopeArgs rope_args(const gqe_config& c, const gqe_rope& r, const void* Q, const void* Qs, const void* K, const void* Qo,
+                   const void* Qso, const void* Ko) {
+  RopeArgs a{};
+  const long long dh = c.d_head, T = c.T;
+  const void* in[3] = {Q, Qs, K};
+  const void* out[3] = {Qo, Qso, Ko};
+  const int heads[3] = {c.G * c.k, 1, c.G};
+  for (int i = 0; i < 3; ++i) {
+    a.n[i] = out[i] != nullptr ? heads[i] : 0;
+    a.x[i] = rope_rows(in[i], heads[i] * T * dh, T * dh, dh);
+    a.y[i] = rope_rows(out[i], heads[i] * T * dh, T * dh, dh);
+  }
+  a.R = static_cast<long long>(c.B) * c.T;
+  a.T = c.T;
+  a.d_rot = r.d_rot;
+  a.axes = r.axes;
+  a.adjacent = (r.flags & GQE_ROPE_ADJACENT) != 0u;
+  a.norm = (r.flags & GQE_ROPE_NORM) != 0u;
+  a.eps = r.eps;
+  a.scale = r.scale;
+  a.pos = r.pos;
+  a.inv_freq = r.inv_freq;
+  a.axis = r.axis;
+  a.w_q = r.w_q;
+  a.w_k = r.w_k;
+  return a;
+}
+
+gqe_status check_decode_kv4(const gqe_config* c) {
+  if (c == nullptr || c->T < 1) return GQE_ERR_INVALID;
+  const gqe_config c1 = decode_rows_cfg(*c);
+  const gqe_status s = check_cfg(&c1);  // B rows; the long extent is the cache
+  if (s != GQE_OK) return s;
+  if ((c->flags & (kOutFlags | GQE_FLAG_NO_SHARED_HEAD | GQE_FLAG_EXPERT_MAJOR)) != 0u || c->k > 15 ||
+      static_cast<long long>(c->B) * c->G > 65535)
+    return GQE_ERR_UNSUPPORTED;
+  return GQE_OK;
+}
+
+gqe_status check_kv4(const gqe_kv4* c) {
+  if (c == nullptr || !all_aligned(c->k_codes, c->v_codes) || !all_aligned(c->meta) || c->capacity < 16 ||
+      c->capacity % 16 != 0)
+    return GQE_ERR_INVALID;
+  return GQE_OK;
+}
+
 // One warp waits, with a bound, on a barrier that nothing completes: the
 // wait gives up after limit_ns and records GQE_ERR_TIMEOUT.
 __global__ void selftest_wait_kernel(uint64_t limit_ns) {
@@ -271,6 +389,18 @@ using namespace gqe;
 extern "C" {
 
 size_t gqe_workspace_bytes(const gqe_config* cfg, int which) {
+  if (which == GQE_WS_QK_ROPE) return check_rows(cfg) != GQE_OK ? 0 : rope_bwd_ws_bytes(cfg->d_head);
+  if (which == GQE_WS_BALANCE) return check_rows(cfg) != GQE_OK ? 0 : balance_ws_bytes(cfg->G * cfg->M);
+  if (which == GQE_WS_KV4) {
+    if (check_shape(cfg) != GQE_OK || cfg->k > 16 || static_cast<long long>(cfg->B) * cfg->G > 65535) return 0;
+    return kv4_attention_ws_bytes(cfg->B, cfg->G, cfg->T, cfg->k + 1, cfg->d_head);
+  }
+  if (which == GQE_WS_DECODE_KV4) {
+    if (check_decode_kv4(cfg) != GQE_OK) return 0;
+    return decode_kv4_ws(*cfg).total;
+  }
+  if (which == GQE_WS_BACKWARD_AUX)
+    return check_cfg(cfg) != GQE_OK || (cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u ? 0 : bwd_aux_ws(*cfg).total;
   if (cfg != nullptr && (which == GQE_WS_DECODE || which == GQE_WS_DENSE_DECODE)) {
     // Decode: the per-token buffers have B rows; T is the cache length.
     gqe_config c1 = decode_rows_cfg(*cfg);
@@ -409,12 +539,20 @@ gqe_status gqe_output_proj(const gqe_config* cfg, gqe_bf16* slots, const float* 
   return cuda_status(gemm_output(*cfg, slots, omega, W_o, y, stream));
 }
 
+// Rotated Q, Qs, K of a layer call that keeps the unrotated ones; null: in place.
+struct RopeOut {
+  gqe_bf16* Qv;
+  gqe_bf16* Qs;
+  gqe_bf16* K;
+};
+
 // The layer forward; lse (optional, slot-major attention only) receives the
-// attention rows' log-sum-exp for the backward.
+// attention rows' log-sum-exp for the backward. rope: optional.
 static gqe_status layer_fwd(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r,
                             const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v,
                             const gqe_bf16* W_o, gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream,
-                            float* lse, bool allow_short) {
+                            float* lse, bool allow_short, const gqe_rope* rope = nullptr,
+                            const RopeOut* rope_out = nullptr) {
   const gqe_status s = check_cfg(cfg);
   if (s != GQE_OK) return s;
   const bool shared = has_shared_head(*cfg);
@@ -482,11 +620,21 @@ static gqe_status layer_fwd(const gqe_config* cfg, const gqe_bf16* x, const floa
     if (side != nullptr && cudaStreamWaitEvent(main_st, side->join, 0) != cudaSuccess)
       return GQE_ERR_CUDA;
   }
-  const int ea = (cfg->flags & GQE_FLAG_EXPERT_MAJOR) != 0u
-                     ? attention_gqe_em(*cfg, H(L.Qv), H(L.Qs), H(L.K), H(L.V), I(L.idx), I(L.offsets),
-                                        I(L.tok), H(L.slots), stream)
-                     : attention_gqe(*cfg, H(L.Qv), H(L.Qs), H(L.K), H(L.V), H(L.slots), w + L.aws,
-                                     L.total - L.aws, true, stream, lse);
+  const bool expert_major = (cfg->flags & GQE_FLAG_EXPERT_MAJOR) != 0u;
+  gqe_bf16 *Qv = H(L.Qv), *Qs = H(L.Qs), *K = H(L.K);
+  if (rope != nullptr) {
+    if (rope_out != nullptr) {
+      Qv = rope_out->Qv;
+      Qs = rope_out->Qs;
+      K = rope_out->K;
+    }
+    RopeArgs a = rope_args(*cfg, *rope, H(L.Qv), H(L.Qs), H(L.K), Qv, shared ? Qs : nullptr, K);
+    if (expert_major) a.slot_pos = I(L.slot_pos);
+    if (rope_fwd(a, cfg->d_head, stream) != cudaSuccess) return GQE_ERR_CUDA;
+  }
+  const int ea = expert_major
+                     ? attention_gqe_em(*cfg, Qv, Qs, K, H(L.V), I(L.idx), I(L.offsets), I(L.tok), H(L.slots), stream)
+                     : attention_gqe(*cfg, Qv, Qs, K, H(L.V), H(L.slots), w + L.aws, L.total - L.aws, true, stream, lse);
   if (ea != cudaSuccess) return GQE_ERR_CUDA;
   return gqe_output_proj(cfg, H(L.slots), F(L.omega), W_o, y, stream);
 }
@@ -498,11 +646,31 @@ gqe_status gqe_layer_fwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
   return layer_fwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, y, ws, ws_bytes, stream, nullptr, true);
 }
 
-gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r,
-                         const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v,
-                         const gqe_bf16* W_o, const float* dy, float* dx, float* dW_r, float* db_r,
-                         float* dW_q, float* dW_qs, float* dW_k, float* dW_v, float* dW_o, void* ws,
-                         size_t ws_bytes, gqe_stream_t stream) {
+gqe_status gqe_layer_fwd_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                              const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                              const gqe_bf16* W_v, const gqe_bf16* W_o, gqe_bf16* y, void* ws, size_t ws_bytes,
+                              gqe_stream_t stream) {
+  gqe_status s = check_cfg(cfg);
+  if (s == GQE_OK) s = check_rope(*cfg, rope);
+  if (s != GQE_OK) return s;
+  return layer_fwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, y, ws, ws_bytes, stream, nullptr, true, rope);
+}
+
+// The layer backward; aux (optional): its workspace part, with the rope
+// (optional) and balance loss (optional) of gqe_layer_bwd_aux.
+struct BwdAux {
+  const gqe_rope* rope;
+  const gqe_balance* balance;
+  float* dw_qn;
+  float* dw_kn;
+  BwdAuxWs A;
+};
+
+static gqe_status layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r,
+                            const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v,
+                            const gqe_bf16* W_o, const float* dy, float* dx, float* dW_r, float* db_r, float* dW_q,
+                            float* dW_qs, float* dW_k, float* dW_v, float* dW_o, void* ws, size_t ws_bytes,
+                            gqe_stream_t stream, const BwdAux* aux) {
   const gqe_status s = check_cfg(cfg);
   if (s != GQE_OK) return s;
   if ((cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u) return GQE_ERR_UNSUPPORTED;  // the default construction only
@@ -512,15 +680,18 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
     return GQE_ERR_INVALID;
   const gqe_config& c = *cfg;
   const BwdWs W = bwd_ws(c);
-  if (ws_bytes < W.total) return GQE_ERR_WORKSPACE;
+  if (ws_bytes < (aux != nullptr ? aux->A.total : W.total)) return GQE_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
   auto Fp = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
   auto Hp = [&](size_t o) { return reinterpret_cast<uint16_t*>(w + o); };
   // The forward, into the layer part of the workspace (routing, Q, K, V, slots).
-  gqe_status st = layer_fwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, reinterpret_cast<gqe_bf16*>(w + W.y), ws,
-                            W.L.total, stream, Fp(W.lse), true);
-  if (st != GQE_OK) return st;
+  const gqe_rope* rope = aux != nullptr ? aux->rope : nullptr;
+  const gqe_balance* bal = aux != nullptr ? aux->balance : nullptr;
   const LayerWs& L = W.L;
+  const RopeOut ro{Hp(rope ? aux->A.Qv : L.Qv), Hp(rope ? aux->A.Qs : L.Qs), Hp(rope ? aux->A.K : L.K)};
+  gqe_status st = layer_fwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, reinterpret_cast<gqe_bf16*>(w + W.y), ws,
+                            W.L.total, stream, Fp(W.lse), true, rope, &ro);
+  if (st != GQE_OK) return st;
   const long long R = static_cast<long long>(c.B) * c.T;
   const int d = c.d_model, dh = c.d_head, gk = c.G * c.k, N = c.G * c.M, Sdh = (gk + 2) * dh;
   const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
@@ -535,6 +706,16 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
   auto U = [](const gqe_bf16* p) { return reinterpret_cast<const uint16_t*>(p); };
   int e = cudaSuccess;
   auto ok = [&](int r) { e = r; return r == cudaSuccess; };
+  auto rope_bwd_layer = [&]() {
+    const long long T = c.T, H = gk + 1;
+    RopeArgs a = rope_args(c, *rope, Hp(L.Qv), Hp(L.Qs), Hp(L.K), Fp(W.dQr), Fp(W.dQs), Fp(W.dS));
+    a.y[0] = rope_rows(Fp(W.dQr), T * gk * dh, dh, static_cast<long long>(gk) * dh);  // [R, G, k, dh]
+    RopeBwdArgs b{};
+    b.g[0] = RopeGrad{a.y[0], 2, 1, R * gk * dh, 0, 0};
+    b.g[1] = RopeGrad{a.y[1], 2, 1, R * dh, 0, 0};
+    b.g[2] = RopeGrad{rope_rows(Fp(W.dKp), H * T * dh, c.k * T * dh, dh), 2, c.k, R * H * dh, T * dh, gk * T * dh};
+    return rope_bwd(a, b, dh, aux->dw_qn, aux->dw_kn, w + aux->A.scratch, stream);
+  };
   // a11: dS = dy W_O^T; dW_O = S^T dy (tensor cores, bf16 operands).
   ok(bwd_cast(dy, d, R, d, dy16, d, stream)) && ok(bwd_transpose(U(W_o), d, Sdh, d, Hp(W.WoT), W.ldS, stream)) &&
       ok(gemm_f32out(dy16, d, Ri, d, Hp(W.WoT), W.ldS, Sdh, Fp(W.dS), Sdh, stream)) &&
@@ -543,14 +724,23 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
       // a10, a4, a2: slots and router -> dO, dz; db = sum dz.
       ok(bwd_slots_router(c, xb, W_r, b_r, Fp(W.zl), reinterpret_cast<const int32_t*>(w + L.idx), Fp(L.omega), slots,
                           Fp(W.dS), Fp(W.dOr), Fp(W.dOs), Fp(W.dz), Hp(W.dO16), Fp(W.Drow), stream)) &&
+      // The balance loss of the layer's routing: its logit gradient joins dz.
+      (bal == nullptr ||
+       (ok(balance_stats(Fp(W.zl), reinterpret_cast<const int32_t*>(w + L.idx), bal->mask, R, c.G, c.M, c.k,
+                         bal->counts, bal->sums, w + aux->A.scratch, stream)) &&
+        ok(balance_grad(Fp(W.zl), bal->mask, bal->counts, bal->sums, R, c.G, c.M, c.k, bal->c_balance, bal->c_z,
+                        bal->loss, Fp(W.dz), true, stream)))) &&
       (db_r == nullptr || ok(bwd_colsum(Fp(W.dz), db_r, R, N, stream))) &&
       // a8: attention -> dq, dK, dV.
-      ok(bwd_attention_tc(c, Hp(L.Qv), Hp(L.Qs), Hp(L.K), Hp(L.V), Hp(W.dO16), Fp(W.Drow), Fp(W.lse), Fp(W.stats),
+      ok(bwd_attention_tc(c, ro.Qv, ro.Qs, ro.K, Hp(L.V), Hp(W.dO16), Fp(W.Drow), Fp(W.lse), Fp(W.stats),
                           Fp(W.dQr), Fp(W.dQs), Fp(W.dKp), Fp(W.dVp), stream)) &&
+      // Back through the norm and rotation: the parts of dQ and dK are added
+      // on the way (dS is done with: its place takes dK).
+      (rope == nullptr || ok(rope_bwd_layer())) &&
       // a7, a6, a1: Y = [dQ (routed, scattered to their experts) | dQs | dK | dV | dz];
       // dx = Y [W_q | W_qs | W_k | W_v | W_r]^T; each weight gradient = x^T (its columns of Y).
       ok(bwd_pack(c, Fp(W.dQr), Fp(W.dQs), Fp(W.dKp), Fp(W.dVp), Fp(W.dz), reinterpret_cast<const int32_t*>(w + L.idx),
-                  Y, static_cast<int>(Kc), stream)) &&
+                  rope != nullptr ? Fp(W.dS) : nullptr, Y, static_cast<int>(Kc), stream)) &&
       ok(bwd_transpose(U(W_q), c1, d, static_cast<int>(c1), WcT, d, stream)) &&
       ok(bwd_transpose(U(W_qs), dh, d, dh, WcT + c1 * d, d, stream)) &&
       ok(bwd_transpose(U(W_k), Gdh, d, Gdh, WcT + c2 * d, d, stream)) &&
@@ -564,6 +754,151 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
       ok(gemm_f32out(Hp(W.xT), W.ldR, d, Ri, Y + c3, Kc, Gdh, dW_v, Gdh, stream)) &&
       ok(gemm_f32out(Hp(W.xT), W.ldR, d, Ri, Y + c4, Kc, N, dW_r, N, stream));
   return cuda_status(e);
+}
+
+gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r,
+                         const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v,
+                         const gqe_bf16* W_o, const float* dy, float* dx, float* dW_r, float* db_r,
+                         float* dW_q, float* dW_qs, float* dW_k, float* dW_v, float* dW_o, void* ws,
+                         size_t ws_bytes, gqe_stream_t stream) {
+  return layer_bwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, dy, dx, dW_r, db_r, dW_q, dW_qs, dW_k, dW_v, dW_o, ws,
+                   ws_bytes, stream, nullptr);
+}
+
+gqe_status gqe_layer_bwd_aux(const gqe_config* cfg, const gqe_rope* rope, const gqe_balance* balance,
+                             const gqe_bf16* x, const float* W_r, const float* b_r, const gqe_bf16* W_q,
+                             const gqe_bf16* W_qs, const gqe_bf16* W_k, const gqe_bf16* W_v, const gqe_bf16* W_o,
+                             const float* dy, float* dx, float* dW_r, float* db_r, float* dW_q, float* dW_qs,
+                             float* dW_k, float* dW_v, float* dW_o, float* dw_qn, float* dw_kn, void* ws,
+                             size_t ws_bytes, gqe_stream_t stream) {
+  gqe_status s = check_cfg(cfg);
+  if (s != GQE_OK) return s;
+  if ((cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u) return GQE_ERR_UNSUPPORTED;
+  if (rope != nullptr && (s = check_rope(*cfg, rope)) != GQE_OK) return s;
+  if ((dw_qn != nullptr || dw_kn != nullptr) && (rope == nullptr || (rope->flags & GQE_ROPE_NORM) == 0u))
+    return GQE_ERR_INVALID;
+  if (!aligned_to(dw_qn, 4) || !aligned_to(dw_kn, 4)) return GQE_ERR_INVALID;
+  if (balance != nullptr && (!all_aligned(balance->counts) || !all_aligned(balance->sums) || !aligned_to(balance->loss, 4)))
+    return GQE_ERR_INVALID;
+  const BwdAux aux{rope, balance, dw_qn, dw_kn, bwd_aux_ws(*cfg)};
+  return layer_bwd(cfg, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, dy, dx, dW_r, db_r, dW_q, dW_qs, dW_k, dW_v, dW_o, ws,
+                   ws_bytes, stream, &aux);
+}
+
+gqe_status gqe_qk_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* Q, const gqe_bf16* Qs,
+                       const gqe_bf16* K, const int32_t* slot_pos, gqe_bf16* Qo, gqe_bf16* Qso, gqe_bf16* Ko,
+                       gqe_stream_t stream) {
+  gqe_status s = check_rows(cfg);
+  if (s == GQE_OK) s = check_rope(*cfg, rope);
+  if (s != GQE_OK) return s;
+  if ((Q == nullptr) != (Qo == nullptr) || (Qs == nullptr) != (Qso == nullptr) || (K == nullptr) != (Ko == nullptr) ||
+      (Q == nullptr && Qs == nullptr && K == nullptr))
+    return GQE_ERR_INVALID;
+  if (!aligned16(Q) || !aligned16(Qs) || !aligned16(K) || !aligned16(Qo) || !aligned16(Qso) || !aligned16(Ko) ||
+      !aligned_to(slot_pos, 4))
+    return GQE_ERR_INVALID;
+  RopeArgs a = rope_args(*cfg, *rope, Q, Qs, K, Qo, Qso, Ko);
+  a.slot_pos = slot_pos;
+  return cuda_status(rope_fwd(a, cfg->d_head, stream));
+}
+
+gqe_status gqe_qk_rope_bwd(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* Q, const gqe_bf16* Qs,
+                           const gqe_bf16* K, const int32_t* slot_pos, const float* dQo, const float* dQso,
+                           const float* dKo, float* dQ, float* dQs, float* dK, float* dw_q, float* dw_k, void* ws,
+                           size_t ws_bytes, gqe_stream_t stream) {
+  gqe_status s = check_rows(cfg);
+  if (s == GQE_OK) s = check_rope(*cfg, rope);
+  if (s != GQE_OK) return s;
+  const bool norm = (rope->flags & GQE_ROPE_NORM) != 0u;
+  const gqe_bf16* in[3] = {Q, Qs, K};
+  const float* g[3] = {dQo, dQso, dKo};
+  float* out[3] = {dQ, dQs, dK};
+  for (int i = 0; i < 3; ++i) {
+    if ((g[i] == nullptr) != (out[i] == nullptr) || (norm && g[i] != nullptr && in[i] == nullptr)) return GQE_ERR_INVALID;
+    if (!aligned16(in[i]) || !aligned16(g[i]) || !aligned16(out[i])) return GQE_ERR_INVALID;
+  }
+  if ((dQ == nullptr && dQs == nullptr && dK == nullptr) || ((dw_q != nullptr || dw_k != nullptr) && !norm) ||
+      !aligned_to(dw_q, 4) || !aligned_to(dw_k, 4) || !aligned_to(slot_pos, 4))
+    return GQE_ERR_INVALID;
+  if (ws == nullptr || !aligned16(ws)) return GQE_ERR_INVALID;
+  if (ws_bytes < rope_bwd_ws_bytes(cfg->d_head)) return GQE_ERR_WORKSPACE;
+  RopeArgs a = rope_args(*cfg, *rope, Q, Qs, K, dQ, dQs, dK);
+  a.slot_pos = slot_pos;
+  RopeBwdArgs b{};
+  for (int i = 0; i < 3; ++i) {
+    b.g[i] = RopeGrad{a.y[i], 1, 1, 0, 0, 0};
+    b.g[i].rows.p = const_cast<float*>(g[i]);
+  }
+  return cuda_status(rope_bwd(a, b, cfg->d_head, dw_q, dw_k, ws, stream));
+}
+
+gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r, float* z,
+                             gqe_stream_t stream) {
+  const gqe_status s = check_cfg(cfg);
+  if (s != GQE_OK) return s;
+  if (!all_aligned(x) || !all_aligned(W_r, static_cast<const float*>(z)) || !aligned_to(b_r, 4)) return GQE_ERR_INVALID;
+  return cuda_status(router_logits(*cfg, x, W_r, b_r, z, stream));
+}
+
+gqe_status gqe_balance_stats(const gqe_config* cfg, const float* z, const int32_t* idx, const uint8_t* mask,
+                             int32_t* counts, float* sums, void* ws, size_t ws_bytes, gqe_stream_t stream) {
+  const gqe_status s = check_rows(cfg);
+  if (s != GQE_OK) return s;
+  if (!all_aligned(z, static_cast<const float*>(sums)) || !all_aligned(idx, static_cast<const int32_t*>(counts)) ||
+      ws == nullptr || !aligned16(ws))
+    return GQE_ERR_INVALID;
+  if (ws_bytes < balance_ws_bytes(cfg->G * cfg->M)) return GQE_ERR_WORKSPACE;
+  return cuda_status(balance_stats(z, idx, mask, static_cast<long long>(cfg->B) * cfg->T, cfg->G, cfg->M, cfg->k, counts,
+                                   sums, ws, stream));
+}
+
+gqe_status gqe_balance_loss(const gqe_config* cfg, const float* z, const uint8_t* mask, const int32_t* counts,
+                            const float* sums, float c_balance, float c_z, float* loss, float* dz, int accumulate,
+                            gqe_stream_t stream) {
+  const gqe_status s = check_rows(cfg);
+  if (s != GQE_OK) return s;
+  if (!all_aligned(counts) || !all_aligned(sums) || !aligned_to(loss, 4) || (loss == nullptr && dz == nullptr) ||
+      (dz != nullptr && !all_aligned(z, static_cast<const float*>(dz))))
+    return GQE_ERR_INVALID;
+  return cuda_status(balance_grad(z, mask, counts, sums, static_cast<long long>(cfg->B) * cfg->T, cfg->G, cfg->M, cfg->k,
+                                  c_balance, c_z, loss, dz, accumulate != 0, stream));
+}
+
+gqe_status gqe_kv4_append(const gqe_config* cfg, const gqe_bf16* K, const gqe_bf16* V, const int32_t* start,
+                          const int32_t* count, const gqe_kv4* cache, gqe_stream_t stream) {
+  gqe_status s = check_rows(cfg);
+  if (s == GQE_OK) s = check_kv4(cache);
+  if (s != GQE_OK) return s;
+  if (!all_aligned(K, V) || !aligned_to(start, 4) || !aligned_to(count, 4)) return GQE_ERR_INVALID;
+  return cuda_status(kv4_append(cfg->B, cfg->G, cfg->T, cfg->d_head, K, V, start, 0, count, *cache, stream));
+}
+
+gqe_status gqe_kv4_read(const gqe_config* cfg, const gqe_kv4* cache, const int32_t* start, const int32_t* count,
+                        gqe_bf16* K, gqe_bf16* V, gqe_stream_t stream) {
+  gqe_status s = check_rows(cfg);
+  if (s == GQE_OK) s = check_kv4(cache);
+  if (s != GQE_OK) return s;
+  if (!all_aligned(K, V) || !aligned_to(start, 4) || !aligned_to(count, 4)) return GQE_ERR_INVALID;
+  return cuda_status(kv4_read(cfg->B, cfg->G, cfg->T, cfg->d_head, *cache, start, count, K, V, stream));
+}
+
+gqe_status gqe_kv4_attention(const gqe_config* cfg, const gqe_bf16* Q, const gqe_bf16* Qs, const gqe_kv4* cache,
+                             const int32_t* lens, gqe_bf16* out, int32_t ldo, void* ws, size_t ws_bytes,
+                             gqe_stream_t stream) {
+  gqe_status s = check_shape(cfg);
+  if (s == GQE_OK) s = check_kv4(cache);
+  if (s != GQE_OK) return s;
+  const int heads = cfg->k + (Qs != nullptr ? 1 : 0);
+  if (cache->capacity < cfg->T || ldo % 8 != 0 ||
+      ldo < (static_cast<long long>(cfg->G) * cfg->k + (Qs != nullptr ? 1 : 0)) * cfg->d_head)
+    return GQE_ERR_INVALID;
+  if (!all_aligned(Q, static_cast<const gqe_bf16*>(out)) || !aligned16(Qs) || !aligned_to(lens, 4) || ws == nullptr ||
+      !aligned16(ws))
+    return GQE_ERR_INVALID;
+  if (heads > 16 || static_cast<long long>(cfg->B) * cfg->G > 65535) return GQE_ERR_UNSUPPORTED;
+  if (ws_bytes < kv4_attention_ws_bytes(cfg->B, cfg->G, cfg->T, heads, cfg->d_head)) return GQE_ERR_WORKSPACE;
+  return cuda_status(kv4_attention(cfg->B, cfg->G, cfg->T, cfg->k, cfg->d_head, Q, Qs, *cache, lens, 0, out, ldo, ws,
+                                   stream));
 }
 
 gqe_status gqa_dense_fwd(const gqe_config* cfg, const gqe_bf16* x, const gqe_bf16* W_q,
@@ -642,11 +977,10 @@ int gqe_version(void) { return 100; }
 
 }  // extern "C"
 
-gqe_status gqe_decode_step(const gqe_config* cfg, const gqe_bf16* x, const float* W_r,
-                           const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs,
-                           const gqe_bf16* W_k, const gqe_bf16* W_v, const gqe_bf16* W_o,
-                           gqe_bf16* K_cache, gqe_bf16* V_cache, int32_t cache_capacity, gqe_bf16* y,
-                           void* ws, size_t ws_bytes, gqe_stream_t stream) {
+static gqe_status decode_step(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                              const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                              const gqe_bf16* W_v, const gqe_bf16* W_o, gqe_bf16* K_cache, gqe_bf16* V_cache,
+                              int32_t cache_capacity, gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream) {
   if (cfg == nullptr || cfg->T < 1) return GQE_ERR_INVALID;
   const gqe_config c1 = decode_rows_cfg(*cfg);
   const gqe_status s = check_cfg(&c1);  // B rows; the long extent is the cache
@@ -673,8 +1007,75 @@ gqe_status gqe_decode_step(const gqe_config* cfg, const gqe_bf16* x, const float
   if (st != GQE_OK) return st;
   if (gemm_kv_at(c1, x, W_k, W_v, K_cache, V_cache, cache_capacity, cfg->T - 1, stream) != cudaSuccess)
     return GQE_ERR_CUDA;
+  if (rope != nullptr) {
+    gqe_bf16* Kn = K_cache + static_cast<size_t>(cfg->T - 1) * cfg->d_head;  // the new keys' rows
+    RopeArgs a = rope_args(c1, *rope, H(L.Qv), H(L.Qs), Kn, H(L.Qv), H(L.Qs), Kn);
+    const long long sh = static_cast<long long>(cache_capacity) * cfg->d_head;
+    a.x[2] = a.y[2] = rope_rows(Kn, cfg->G * sh, sh, cfg->d_head);
+    a.pos0 = cfg->T - 1;
+    if (rope_fwd(a, cfg->d_head, stream) != cudaSuccess) return GQE_ERR_CUDA;
+  }
   if (decode_attention(*cfg, false, H(L.Qv), H(L.Qs), K_cache, V_cache, cache_capacity, H(L.slots),
                        (cfg->G * cfg->k + 2) * cfg->d_head, w + D.daws, stream) != cudaSuccess)
+    return GQE_ERR_CUDA;
+  return gqe_output_proj(&c1, H(L.slots), F(L.omega), W_o, y, stream);
+}
+
+gqe_status gqe_decode_step(const gqe_config* cfg, const gqe_bf16* x, const float* W_r,
+                           const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs,
+                           const gqe_bf16* W_k, const gqe_bf16* W_v, const gqe_bf16* W_o,
+                           gqe_bf16* K_cache, gqe_bf16* V_cache, int32_t cache_capacity, gqe_bf16* y,
+                           void* ws, size_t ws_bytes, gqe_stream_t stream) {
+  return decode_step(cfg, nullptr, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, K_cache, V_cache, cache_capacity, y, ws,
+                     ws_bytes, stream);
+}
+
+gqe_status gqe_decode_step_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                                const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                                const gqe_bf16* W_v, const gqe_bf16* W_o, gqe_bf16* K_cache, gqe_bf16* V_cache,
+                                int32_t cache_capacity, gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream) {
+  if (cfg == nullptr) return GQE_ERR_INVALID;
+  const gqe_status s = check_rope(*cfg, rope);
+  if (s != GQE_OK) return s;
+  if ((cfg->flags & GQE_FLAG_EXPERT_MAJOR) != 0u) return GQE_ERR_UNSUPPORTED;
+  return decode_step(cfg, rope, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, K_cache, V_cache, cache_capacity, y, ws,
+                     ws_bytes, stream);
+}
+
+gqe_status gqe_decode_step_kv4(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* x, const float* W_r,
+                               const float* b_r, const gqe_bf16* W_q, const gqe_bf16* W_qs, const gqe_bf16* W_k,
+                               const gqe_bf16* W_v, const gqe_bf16* W_o, const gqe_kv4* cache, const int32_t* lens,
+                               gqe_bf16* y, void* ws, size_t ws_bytes, gqe_stream_t stream) {
+  gqe_status s = check_decode_kv4(cfg);
+  if (s == GQE_OK) s = check_kv4(cache);
+  if (s == GQE_OK && rope != nullptr) s = check_rope(*cfg, rope);
+  if (s != GQE_OK) return s;
+  if (cache->capacity < cfg->T || !all_aligned(x, W_q, W_qs, W_k, W_v, W_o) ||
+      !all_aligned(W_r) || !all_aligned(y) || !aligned_to(b_r, 4) || !aligned_to(lens, 4) || ws == nullptr || !aligned16(ws))
+    return GQE_ERR_INVALID;
+  const gqe_config c1 = decode_rows_cfg(*cfg);
+  const DecodeKv4Ws D = decode_kv4_ws(*cfg);
+  if (ws_bytes < D.total) return GQE_ERR_WORKSPACE;
+  const LayerWs& L = D.L1;
+  char* w = static_cast<char*>(ws);
+  auto I = [&](size_t o) { return reinterpret_cast<int32_t*>(w + o); };
+  auto F = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
+  auto H = [&](size_t o) { return reinterpret_cast<gqe_bf16*>(w + o); };
+  s = gqe_router_topk(&c1, x, W_r, b_r, I(L.idx), F(L.r), F(L.omega), stream);
+  if (s != GQE_OK) return s;
+  s = gqe_dispatch(&c1, I(L.idx), x, W_q, W_qs, I(L.counts), I(L.offsets), I(L.tok), I(L.slot_pos), H(L.Qv), H(L.Qs),
+                   w + L.dws, L.aws - L.dws, stream);
+  if (s != GQE_OK) return s;
+  if (gemm_kv(c1, x, W_k, W_v, H(L.K), H(L.V), stream) != cudaSuccess) return GQE_ERR_CUDA;
+  if (rope != nullptr) {
+    RopeArgs a = rope_args(c1, *rope, H(L.Qv), H(L.Qs), H(L.K), H(L.Qv), H(L.Qs), H(L.K));
+    a.pos0 = lens != nullptr ? 0 : cfg->T - 1;
+    a.pos_len = lens;
+    if (rope_fwd(a, cfg->d_head, stream) != cudaSuccess) return GQE_ERR_CUDA;
+  }
+  if (kv4_append(c1.B, c1.G, 1, c1.d_head, H(L.K), H(L.V), lens, cfg->T - 1, nullptr, *cache, stream) != cudaSuccess ||
+      kv4_attention(cfg->B, cfg->G, cfg->T, cfg->k, cfg->d_head, H(L.Qv), H(L.Qs), *cache, lens, 1, H(L.slots),
+                    (cfg->G * cfg->k + 2) * cfg->d_head, w + D.aws, stream) != cudaSuccess)
     return GQE_ERR_CUDA;
   return gqe_output_proj(&c1, H(L.slots), F(L.omega), W_o, y, stream);
 }

@@ -257,14 +257,14 @@ __global__ void cast_kernel(const float* in, long long ldi, long long rows, int 
 // dz | 0 padding]. dK and dV of group g are the sums, in stream order, of the
 // per-stream parts dKp, dVp [B, G k + 1, T, dh] of its k routed streams (and
 // of the shared head for group 0); each of dQ, dK, dV arrives in two parts
-// [2][...] that are added here. Each thread writes 8 adjacent columns;
-// the segment bounds before dz are multiples of 32, so 8 columns never
+// [2][...] that are added here (dKc non-null: dQ and dK are sums already, dK
+// in dKc [B, G, T, dh]). Each thread writes 8 adjacent columns; the segment bounds before dz are multiples of 32, so 8 columns never
 // straddle two of them.
 __global__ void pack_grads_kernel(const float* dQr, const float* dQs, const float* dKp, const float* dVp,
-                                  const float* dz, const int32_t* idx, uint16_t* Y, long long R, int T, int G,
-                                  int M, int k, int dh, int ld) {
+                                  const float* dz, const int32_t* idx, const float* dKc, uint16_t* Y, long long R,
+                                  int T, int G, int M, int k, int dh, int ld) {
   const int N = G * M, gk = G * k, c1 = N * dh, c2 = c1 + dh, c3 = c2 + G * dh, c4 = c3 + G * dh, c5 = c4 + N;
-  const int per_row = ld / 8;
+  const int per_row = ld / 8, q_parts = dKc != nullptr ? 1 : 2;
   const long long n = R * per_row;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
@@ -286,15 +286,16 @@ __global__ void pack_grads_kernel(const float* dQr, const float* dQs, const floa
       const int32_t* ip = idx + (r * G + g) * k;
       for (int s = 0; s < k; ++s)
         if (ip[s] == j)
-          for (int hf = 0; hf < 2; ++hf) add8(dQr + hf * R * gk * dh + ((r * G + g) * k + s) * dh + col);
+          for (int hf = 0; hf < q_parts; ++hf) add8(dQr + hf * R * gk * dh + ((r * G + g) * k + s) * dh + col);
     } else if (c < c2) {
-      for (int hf = 0; hf < 2; ++hf) add8(dQs + hf * R * dh + r * dh + (c - c1));
+      for (int hf = 0; hf < q_parts; ++hf) add8(dQs + hf * R * dh + r * dh + (c - c1));
     } else if (c < c4) {
       const bool is_k = c < c3;
       const int x = c - (is_k ? c2 : c3), g = x / dh, col = x - g * dh;
       const float* part = is_k ? dKp : dVp;
       const long long half_sz = R * (gk + 1) * dh;
-      for (int hf = 0; hf < 2; ++hf) {
+      if (is_k && dKc != nullptr) add8(dKc + ((bb * G + g) * T + t) * dh + col);
+      else for (int hf = 0; hf < 2; ++hf) {
         for (int s = 0; s < k; ++s) add8(part + hf * half_sz + ((bb * (gk + 1) + g * k + s) * T + t) * dh + col);
         if (g == 0) add8(part + hf * half_sz + ((bb * (gk + 1) + gk) * T + t) * dh + col);
       }
@@ -359,10 +360,21 @@ int bwd_cast(const float* in, long long ldi, long long rows, int cols, uint16_t*
 }
 
 int bwd_pack(const gqe_config& c, const float* dQr, const float* dQs, const float* dKp, const float* dVp,
-             const float* dz, const int32_t* idx, uint16_t* Y, int ld, void* stream) {
+             const float* dz, const int32_t* idx, const float* dKc, uint16_t* Y, int ld, void* stream) {
   const long long R = static_cast<long long>(c.B) * c.T;
-  pack_grads_kernel<<<1184, 256, 0, static_cast<cudaStream_t>(stream)>>>(dQr, dQs, dKp, dVp, dz, idx, Y, R, c.T,
+  pack_grads_kernel<<<1184, 256, 0, static_cast<cudaStream_t>(stream)>>>(dQr, dQs, dKp, dVp, dz, idx, dKc, Y, R, c.T,
                                                                          c.G, c.M, c.k, c.d_head, ld);
+  return cudaGetLastError();
+}
+
+int router_logits(const gqe_config& c, const uint16_t* x, const float* W_r, const float* b_r, float* z, void* stream) {
+  const long long R = static_cast<long long>(c.B) * c.T;
+  const int N = c.G * c.M;
+  const int smem = c.d_model * N * static_cast<int>(sizeof(float)) + kLogitRows * c.d_model * 2;
+  cudaError_t e = static_cast<cudaError_t>(ensure_smem<logits_kernel>(smem));
+  if (e != cudaSuccess) return e;
+  logits_kernel<<<static_cast<unsigned>((R + kLogitRows - 1) / kLogitRows), 256, smem,
+                  static_cast<cudaStream_t>(stream)>>>(x, W_r, b_r, z, R, c.d_model, N);
   return cudaGetLastError();
 }
 
@@ -370,18 +382,11 @@ int bwd_slots_router(const gqe_config& c, const uint16_t* x, const float* W_r, c
                      const int32_t* idx, const float* omega, const uint16_t* slots, const float* dS, float* dOr,
                      float* dOs, float* dz, uint16_t* dO16, float* Drow, void* stream) {
   const long long R = static_cast<long long>(c.B) * c.T;
-  const int N = c.G * c.M;
-  const int smem = c.d_model * N * static_cast<int>(sizeof(float)) + kLogitRows * c.d_model * 2;
-  cudaError_t e = static_cast<cudaError_t>(ensure_smem<logits_kernel>(smem));
-  if (e != cudaSuccess) return e;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  logits_kernel<<<static_cast<unsigned>((R + kLogitRows - 1) / kLogitRows), 256, smem, st>>>(x, W_r, b_r, zl, R,
-                                                                                           c.d_model, N);
-  e = cudaGetLastError();
+  const int e = router_logits(c, x, W_r, b_r, zl, stream);
   if (e != cudaSuccess) return e;
   SlotArgs a{x,  W_r, b_r,       zl,  idx,    omega,  slots,    dS,      dOr, dOs, dz,
              dO16, Drow, c.d_model, c.G, c.M, c.k, c.d_head, c.T, (c.T + 63) / 64 * 64};
-  slot_router_bwd_kernel<<<static_cast<unsigned>(R), 256, 0, st>>>(a);
+  slot_router_bwd_kernel<<<static_cast<unsigned>(R), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError();
 }
 

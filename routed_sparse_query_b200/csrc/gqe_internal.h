@@ -178,8 +178,10 @@ int gemm_f32out(const uint16_t* A, long long lda, int M, int K, const uint16_t* 
 template <typename TI>
 int bwd_transpose(const TI* in, long long ldi, int rows, int cols, uint16_t* out, long long ldo, void* stream);
 int bwd_cast(const float* in, long long ldi, long long rows, int cols, uint16_t* out, long long ldo, void* stream);
+// dKc (optional): dK already summed per group, [B, G, T, dh]; dQr and dQs then
+// hold their sums in their first part.
 int bwd_pack(const gqe_config& c, const float* dQr, const float* dQs, const float* dKp, const float* dVp,
-             const float* dz, const int32_t* idx, uint16_t* Y, int ld, void* stream);
+             const float* dz, const int32_t* idx, const float* dKc, uint16_t* Y, int ld, void* stream);
 // zl: [B*T, G*M] fp32 scratch for the router logits.
 int bwd_slots_router(const gqe_config& c, const uint16_t* x, const float* W_r, const float* b_r, float* zl,
                      const int32_t* idx, const float* omega, const uint16_t* slots, const float* dS, float* dOr,
@@ -193,6 +195,67 @@ int bwd_attention_tc(const gqe_config& c, const uint16_t* Qv, const uint16_t* Qs
                      const uint16_t* V, const uint16_t* dO16, const float* Drow, const float* lse, float* stats,
                      float* dQr, float* dQs, float* dKp, float* dVp, void* stream);
 int bwd_colsum(const float* dz, float* db, long long R, int N, void* stream);
+// Router logits z [R, N] in fp32 (backward.cu).
+int router_logits(const gqe_config& c, const uint16_t* x, const float* W_r, const float* b_r, float* z, void* stream);
+
+// Query/key norm and rotation (rope.cu). Rows of one operand: element 0 of
+// head h at token (b, t) is p[b sb + h sh + t st].
+struct RopeRows {
+  void* p;
+  long long sb, sh, st;
+};
+struct RopeArgs {
+  RopeRows x[3], y[3];      // 0: routed queries, 1: shared head, 2: keys (bf16; y fp32 in the backward)
+  int n[3];                 // heads of each (0: absent)
+  const int32_t* slot_pos;  // routed queries in token-list order: their rows, or null
+  long long R;
+  int T;
+  int d_rot, axes, adjacent, norm;
+  float eps, scale;
+  const int32_t* pos;       // [axes, R], or null: t + pos0 + max(pos_len[b], 0)
+  int pos0;
+  const int32_t* pos_len;
+  const double* inv_freq;   // [d_rot / 2]
+  const int32_t* axis;      // [d_rot / 2] or null
+  const float* w_q;         // [d_head] or null
+  const float* w_k;
+  int hpc;                  // heads per CTA (set by the launcher)
+};
+// A gradient in parts: the sum over f < parts, s < streams of
+// rows[f part_stride + s stream_stride]; head 0 takes, per f, also the row
+// `extra` elements further (0: none).
+struct RopeGrad {
+  RopeRows rows;
+  int parts, streams;
+  long long part_stride, stream_stride, extra;
+};
+struct RopeBwdArgs {
+  RopeGrad g[3];
+  float* part;  // [CTAs][2][d_head] partial weight gradients (set by the launcher)
+};
+constexpr int kRopeCtas = 148 * 8;  // CTAs of 256 threads that fill the SMs
+int rope_fwd(RopeArgs a, int dh, void* stream);
+size_t rope_bwd_ws_bytes(int dh);
+int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* ws, void* stream);
+
+// Balance loss of the router (balance.cu).
+size_t balance_ws_bytes(int N);
+int balance_stats(const float* z, const int32_t* idx, const uint8_t* mask, long long R, int G, int M, int k,
+                  int32_t* counts, float* sums, void* ws, void* stream);
+int balance_grad(const float* z, const uint8_t* mask, const int32_t* counts, const float* sums, long long R, int G,
+                 int M, int k, float c_balance, float c_z, float* loss, float* dz, bool accumulate, void* stream);
+
+// 4-bit cache (kv4.cu).
+// Position of row t: (start ? start[b] : start0) + t.
+int kv4_append(int B, int G, int T, int dh, const uint16_t* K, const uint16_t* V, const int32_t* start, int start0,
+               const int32_t* count, const gqe_kv4& cache, void* stream);
+int kv4_read(int B, int G, int T, int dh, const gqe_kv4& cache, const int32_t* start, const int32_t* count,
+             uint16_t* K, uint16_t* V, void* stream);
+size_t kv4_attention_ws_bytes(int B, int G, int T, int H, int dh);
+// k routed heads per group (Q [B][G][k][dh]) and, with Qs, the shared head in
+// group 0; keys of sequence b: clamp(lens[b] + len_add, 0, T) (lens null: T).
+int kv4_attention(int B, int G, int T, int k, int dh, const uint16_t* Q, const uint16_t* Qs, const gqe_kv4& cache,
+                  const int32_t* lens, int len_add, uint16_t* out, int ldo, void* ws, void* stream);
 
 // Decode step. cfg.T = keys after the step (the new token sits at T - 1),
 // cap = cache capacity per (sequence, group). K/V projection of the new

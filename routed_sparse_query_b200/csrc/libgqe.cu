@@ -5,6 +5,9 @@
 #include "gemm.cu"
 #include "attention.cu"
 #include "decode.cu"
+#include "rope.cu"
+#include "balance.cu"
+#include "kv4.cu"
 #include "api.cu"
 #include "noalloc.cu"
 #include "backward.cu"
