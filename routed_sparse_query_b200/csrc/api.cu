@@ -252,7 +252,7 @@ DecodeKv4Ws decode_kv4_ws(const gqe_config& c) {
   DecodeKv4Ws D{};
   D.L1 = layer_ws(decode_rows_cfg(c));
   D.aws = round256(D.L1.total);
-  D.total = D.aws + kv4_attention_ws_bytes(c.B, c.G, c.T, c.k + 1, c.d_head);
+  D.total = D.aws + kv4_attention_ws_bytes(c.B, c.G, c.k + 1, c.d_head);
   return D;
 }
 
@@ -393,7 +393,7 @@ size_t gqe_workspace_bytes(const gqe_config* cfg, int which) {
   if (which == GQE_WS_BALANCE) return check_rows(cfg) != GQE_OK ? 0 : balance_ws_bytes(cfg->G * cfg->M);
   if (which == GQE_WS_KV4) {
     if (check_shape(cfg) != GQE_OK || cfg->k > 16 || static_cast<long long>(cfg->B) * cfg->G > 65535) return 0;
-    return kv4_attention_ws_bytes(cfg->B, cfg->G, cfg->T, cfg->k + 1, cfg->d_head);
+    return kv4_attention_ws_bytes(cfg->B, cfg->G, cfg->k + 1, cfg->d_head);
   }
   if (which == GQE_WS_DECODE_KV4) {
     if (check_decode_kv4(cfg) != GQE_OK) return 0;
@@ -896,7 +896,7 @@ gqe_status gqe_kv4_attention(const gqe_config* cfg, const gqe_bf16* Q, const gqe
       !aligned16(ws))
     return GQE_ERR_INVALID;
   if (heads > 16 || static_cast<long long>(cfg->B) * cfg->G > 65535) return GQE_ERR_UNSUPPORTED;
-  if (ws_bytes < kv4_attention_ws_bytes(cfg->B, cfg->G, cfg->T, heads, cfg->d_head)) return GQE_ERR_WORKSPACE;
+  if (ws_bytes < kv4_attention_ws_bytes(cfg->B, cfg->G, heads, cfg->d_head)) return GQE_ERR_WORKSPACE;
   return cuda_status(kv4_attention(cfg->B, cfg->G, cfg->T, cfg->k, cfg->d_head, Q, Qs, *cache, lens, 0, out, ldo, ws,
                                    stream));
 }

@@ -251,7 +251,7 @@ int kv4_append(int B, int G, int T, int dh, const uint16_t* K, const uint16_t* V
                const int32_t* count, const gqe_kv4& cache, void* stream);
 int kv4_read(int B, int G, int T, int dh, const gqe_kv4& cache, const int32_t* start, const int32_t* count,
              uint16_t* K, uint16_t* V, void* stream);
-size_t kv4_attention_ws_bytes(int B, int G, int T, int H, int dh);
+size_t kv4_attention_ws_bytes(int B, int G, int H, int dh);
 // k routed heads per group (Q [B][G][k][dh]) and, with Qs, the shared head in
 // group 0; keys of sequence b: clamp(lens[b] + len_add, 0, T) (lens null: T).
 int kv4_attention(int B, int G, int T, int k, int dh, const uint16_t* Q, const uint16_t* Qs, const gqe_kv4& cache,

@@ -169,24 +169,31 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    softmax does per key is done once per lane and not twice.
 //  - A transposed 8 x 8 move turns the weights from (key, head) to the second
 //    product's (head, keys) order.
-// Each warp streams its own tiles of 64 keys of the CTA's span by bulk copies
-// through a ring of its own (no CTA-wide barrier in the loop) and keeps its
-// own running maximum; the warps' states are joined at the end of the span
-// and, with more than one span per sequence and group, by a second kernel.
+// The work is cut over warps: the tiles of 64 keys of all (sequence, group)
+// units, laid end to end, are dealt in equal contiguous shares, so that ragged
+// lengths, few long sequences and many short ones all fill the SMs alike. A
+// warp streams its tiles by bulk copies through a ring of its own, across the
+// units' borders, with its own running maximum and no CTA-wide barrier in the
+// loop. A unit that lies in one warp's share is written out by it; the parts
+// of the others are joined by a second kernel.
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kTile = 64;   // keys per warp tile
+constexpr int kTile = 64;   // keys per tile
 constexpr int kStages = 3;  // tiles in flight per warp
-constexpr int kMinSpan = kTile * kAttnWarps;
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kMaxAttnWarps = 148 * kAttnCtasPerSm * kAttnWarps;
 
 struct AttnArgs {
   const uint16_t* Q;   // [B][G][k][dh]
   const uint16_t* Qs;  // [B][dh] or null
   gqe_kv4 c;
   const int32_t* lens;
-  int len_add, B, G, T, k, H, spans, span;
-  float* part_o;       // [B][G][spans][H][dh]
-  float2* part_ml;     // [B][G][spans][H]
+  int len_add, B, G, T, k, H;
+  // Part of warp w and unit u = b G + g: slot w + u (along the shares, w + u
+  // grows with every part, and a unit's parts are consecutive).
+  float* part_o;       // [slots][H][dh]
+  float2* part_ml;     // [slots][H]: max, sum
+  long long* starts;   // [B + 1]: tiles before sequence b; then the share
   uint16_t* out;
   int ldo;
   float scale_log2;
@@ -196,13 +203,13 @@ __device__ __forceinline__ int keys_of(const AttnArgs& a, int b) {
   const long long n = a.lens != nullptr ? static_cast<long long>(a.lens[b]) + a.len_add : a.T;
   return static_cast<int>(n < 0 ? 0 : n > a.T ? a.T : n);
 }
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 __device__ __forceinline__ int heads_of_group(const AttnArgs& a, int g) { return a.k + (g == 0 && a.Qs != nullptr ? 1 : 0); }
 __device__ __forceinline__ const uint16_t* query_row(const AttnArgs& a, int b, int g, int h, int dh) {
   return h < a.k ? a.Q + ((static_cast<long long>(b) * a.G + g) * a.k + h) * dh : a.Qs + static_cast<long long>(b) * dh;
 }
-__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int g, int h, int d, int dh, float v) {
-  const int col = h < a.k ? g * a.k + h : a.G * a.k;
-  a.out[static_cast<long long>(b) * a.ldo + col * dh + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+__device__ __forceinline__ uint16_t* out_row(const AttnArgs& a, int b, int g, int h, int dh) {
+  return a.out + static_cast<long long>(b) * a.ldo + (h < a.k ? g * a.k + h : a.G * a.k) * dh;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -224,6 +231,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
+// 2^x; results below 2^-126 are 0 (weights that far under the largest are lost
+// in fp32 sums anyway).
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // Row r of a 16-key block holds key row_key(r): the order that keeps both the
 // K reads (rows 0..3 and 4..7 together) and the V reads (even rows, odd rows
@@ -235,122 +250,99 @@ struct AttnShape {
   static constexpr int ROW = DH / 2;                       // bytes of a row's codes
   static constexpr int TILE_BYTES = kTile * (2 * ROW + 8);  // K, V, meta
   static constexpr int RING = kStages * TILE_BYTES;
-  static constexpr int STATE = DH + 2;                     // floats of one head's state
-  static constexpr size_t smem(int H) {
-    const size_t ring = static_cast<size_t>(kAttnWarps) * RING, st = static_cast<size_t>(kAttnWarps) * H * STATE * 4;
-    return (ring > st ? ring : st) + kAttnWarps * kStages * 8 + 16;
+  static constexpr size_t smem() { return static_cast<size_t>(kAttnWarps) * (RING + kStages * 8) + 16; }
+};
+
+// A place in the units' tiles.
+struct Cursor {
+  int b, g, t, n;  // sequence, group, tile of the unit, keys of the sequence
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    if (++t < tiles_of(n)) return;
+    t = 0;
+    if (++g < a.G) return;
+    g = 0;
+    do ++b;
+    while (b < a.B && (n = keys_of(a, b)) == 0);
   }
 };
 
 // HPL: heads per lane (1: even columns, at most 4 heads; 2: all columns);
 // NB: column blocks of 8 (2 only with HPL = 2).
 template <int DH, int HPL, int NB>
-__global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
+struct Warp {
   using S = AttnShape<DH>;
-  constexpr int KS = DH / 16;  // k steps of the scores
-  constexpr int MT = DH / 16;  // 16-row blocks of the output
-  extern __shared__ __align__(128) uint8_t sm[];
-  const int span = blockIdx.x, g = blockIdx.y % a.G, b = blockIdx.y / a.G;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lr = lane >> 2, lc = lane & 3;
-  const size_t state_bytes = static_cast<size_t>(kAttnWarps) * a.H * S::STATE * 4;
-  const size_t data = static_cast<size_t>(kAttnWarps) * S::RING > state_bytes ? static_cast<size_t>(kAttnWarps) * S::RING : state_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + data);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kAttnWarps * kStages);
-  if (tid < kAttnWarps * kStages) mbar_init(bars + tid, 1u);
-  if (tid == 0) *abort_flag = 0;
-  fence_barrier_init();
-  pdl_wait();  // q, lens and the newest rows come from earlier kernels
-  pdl_launch_dependents();
-  __syncthreads();
-  const int n = keys_of(a, b), k0 = span * a.span;
-  if (k0 >= n) {
-    if (n == 0 && span == 0)
-      for (int i = tid; i < heads_of_group(a, g) * DH; i += kAttnThreads) store_out(a, b, g, i / DH, i % DH, DH, 0.0f);
-    return;
-  }
-  const int H = heads_of_group(a, g);
-  const int k1 = min(n, k0 + a.span), tiles = (k1 - k0 + kTile - 1) / kTile;
-  const long long row0 = (static_cast<long long>(b) * a.G + g) * a.c.capacity + k0;
-
-  uint8_t* ring = sm + warp * S::RING;
-  uint64_t* full = bars + warp * kStages;
-  // Tile i of this warp: keys k0 + (warp + 8 i) 64 ..., at most to k1 (rounded
-  // up to an even count: 16-byte pieces; the capacity is a multiple of 16).
-  auto issue = [&](int i) {
-    const int t = (warp + kAttnWarps * i) * kTile;
-    const int nk = (min(kTile, k1 - k0 - t) + 1) & ~1;
-    uint8_t* s = ring + (i % kStages) * S::TILE_BYTES;
-    uint64_t* bar = full + i % kStages;
-    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nk) * (2 * S::ROW + 8));
-    bulk_load(s, a.c.k_codes + (row0 + t) * S::ROW, nk * S::ROW, bar);
-    bulk_load(s + kTile * 2 * S::ROW, a.c.meta + (row0 + t) * 4, nk * 8, bar);
-    bulk_load(s + kTile * S::ROW, a.c.v_codes + (row0 + t) * S::ROW, nk * S::ROW, bar);
-  };
-  const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
-  if (lane == 0)
-    for (int i = 0; i < min(mine, kStages); ++i) issue(i);
-
-  // Queries: this lane's B fragments (column lr of each block), their sums.
-  uint32_t qf[NB][KS][2];
-  float fac[NB][HPL], qsum[NB][HPL];  // of this lane's score columns
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int h = HPL == 1 ? ((lr & 1) ? H : lr >> 1) : nb * 8 + lr;
-    // Lane (lr, lc) holds words 2 lc, 2 lc + 1 of a 64-element row, word lc of a 32-element one.
-    float v[DH / 4], mx = 0.0f, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DH / 4; ++i) {
-      v[i] = h < H ? bf16_f(query_row(a, b, g, h, DH)[lc * (DH / 4) + i]) : 0.0f;
-      mx = fmaxf(mx, fabsf(v[i]));
-      sum += v[i];
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const int e = mx > 0.0f && mx < INFINITY ? ilogbf(mx) : 0;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      // Step s: word s / 2, elements 2 (s % 2) + {0, 4} and, 16 times, {1, 5}.
-      const int i = 8 * (s / 2) + 2 * (s % 2);
-      const __half2 lo = __floats2half2_rn(scalbnf(v[i], 14 - e), scalbnf(v[i + 4], 14 - e));
-      const __half2 hi = __floats2half2_rn(scalbnf(v[i + 1], 10 - e), scalbnf(v[i + 5], 10 - e));
-      qf[nb][s][0] = *reinterpret_cast<const uint32_t*>(&lo);
-      qf[nb][s][1] = *reinterpret_cast<const uint32_t*>(&hi);
-    }
-    // Score columns 2 lc (and 2 lc + 1): their factors from the lanes that formed them.
-    const float f = scalbnf(a.scale_log2, 24 - 14 + e);
-#pragma unroll
-    for (int j = 0; j < HPL; ++j) {
-      fac[nb][j] = __shfl_sync(0xffffffffu, f, (2 * lc + j) * 4);
-      qsum[nb][j] = __shfl_sync(0xffffffffu, sum * a.scale_log2, (2 * lc + j) * 4);
-    }
-  }
-
+  static constexpr int KS = DH / 16;  // k steps of the scores
+  static constexpr int MT = DH / 16;  // 16-row blocks of the output
+  static constexpr int SUB = kTile / 16;
+  uint32_t qf[NB][KS][2];               // B fragments of the queries (column lr)
+  float fac[NB][HPL], qsum[NB][HPL];    // of this lane's score columns
   float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4], ones[NB][4];
+  int lr, lc;
+
+  __device__ __forceinline__ void start(const AttnArgs& a, int b, int g) {
+    const int H = heads_of_group(a, g);
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
+    for (int nb = 0; nb < NB; ++nb) {
+      const int h = HPL == 1 ? ((lr & 1) ? H : lr >> 1) : nb * 8 + lr;
+      // Lane (lr, lc) holds words 2 lc, 2 lc + 1 of a 64-element row, word lc of a 32-element one.
+      float v[DH / 4], mx = 0.0f, sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < HPL; ++j) {
-      m[nb][j] = -INFINITY;
-      l[nb][j] = zs[nb][j] = 0.0f;
-    }
+      for (int i = 0; i < DH / 4; i += 8) {
+        const uint4 w = h < H ? __ldg(reinterpret_cast<const uint4*>(query_row(a, b, g, h, DH) + lc * (DH / 4) + i))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ones[nb][i] = 0.0f;
+        for (int q = 0; q < 4; ++q) {
+          v[i + 2 * q] = __uint_as_float(u[q] << 16);
+          v[i + 2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+        }
+      }
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[nb][t][i] = 0.0f;
+      for (int i = 0; i < DH / 4; ++i) {
+        mx = fmaxf(mx, fabsf(v[i]));
+        sum += v[i];
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
+      // e: the exponent of the largest element (infinities and NaN pass as they are).
+      const int e = mx < INFINITY ? max((__float_as_int(mx) >> 23) - 127, -100) : 0;
+      const float up = pow2(14 - e), up16 = pow2(10 - e);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        // Step s: word s / 2, elements 2 (s % 2) + {0, 4} and, 16 times, {1, 5}.
+        const int i = 8 * (s / 2) + 2 * (s % 2);
+        const __half2 lo = __floats2half2_rn(v[i] * up, v[i + 4] * up);
+        const __half2 hi = __floats2half2_rn(v[i + 1] * up16, v[i + 5] * up16);
+        qf[nb][s][0] = *reinterpret_cast<const uint32_t*>(&lo);
+        qf[nb][s][1] = *reinterpret_cast<const uint32_t*>(&hi);
+      }
+      // Score columns 2 lc (and 2 lc + 1): their factors from the lanes that formed them.
+      const float f = a.scale_log2 * pow2(e) * 1024.0f;  // 2^(24 - 14 + e)
+#pragma unroll
+      for (int j = 0; j < HPL; ++j) {
+        fac[nb][j] = __shfl_sync(0xffffffffu, f, (2 * lc + j) * 4);
+        qsum[nb][j] = __shfl_sync(0xffffffffu, sum * a.scale_log2, (2 * lc + j) * 4);
+        m[nb][j] = -INFINITY;
+        l[nb][j] = zs[nb][j] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ones[nb][i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[nb][t][i] = 0.0f;
+      }
     }
   }
-  const int kr = row_key(lr), v0 = row_key(2 * lc), v1 = row_key(2 * lc + 1);
-  constexpr int SUB = kTile / 16;
-  for (int i = 0; i < mine; ++i) {
-    if (!__all_sync(0xffffffffu, mbar_wait(full + i % kStages, (i / kStages) & 1, abort_flag))) break;
-    const uint8_t* tk = ring + (i % kStages) * S::TILE_BYTES;
+
+  // One tile in shared memory; FULL: 64 keys, else the first `left`.
+  template <bool FULL>
+  __device__ __forceinline__ void tile(const uint8_t* tk, int left) {
     const uint8_t* tv = tk + kTile * S::ROW;
     const uint8_t* tm = tv + kTile * S::ROW;
-    const int left = k1 - k0 - (warp + kAttnWarps * i) * kTile;  // keys of this tile and beyond
+    const int kr = row_key(lr), v0 = row_key(2 * lc), v1 = row_key(2 * lc + 1);
     float sc[NB][SUB][4];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
@@ -392,7 +384,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
       for (int r = 0; r < 2; ++r) {
         const int key = 16 * u + kr + 8 * r;
         const uint2 mm = *reinterpret_cast<const uint2*>(tm + key * 8);
-        const bool on = key < left;
+        const bool on = FULL || key < left;
         const float ks = bf16_f(mm.x & 0xffffu), kz = __uint_as_float(mm.x & 0xffff0000u);
         mv[u][r] = on ? mm.y : 0u;
 #pragma unroll
@@ -414,7 +406,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
         for (int o = 4; o < 32; o <<= 1) mt[nb][j] = fmaxf(mt[nb][j], __shfl_xor_sync(0xffffffffu, mt[nb][j], o));
         const float mn = fmaxf(m[nb][j], mt[nb][j]);
         grown = grown || mn > m[nb][j];
-        al[nb][j] = m[nb][j] == mn ? 1.0f : exp2f(m[nb][j] - mn);
+        al[nb][j] = m[nb][j] == mn ? 1.0f : exp2_ftz(m[nb][j] - mn);
         m[nb][j] = mn;
         mt[nb][j] = mn == -INFINITY ? 0.0f : mn;  // nothing but -inf so far: weights 0
       }
@@ -445,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
           float w2[2] = {0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < HPL; ++j) {
-            const float p = exp2f(sc[nb][u][2 * r + j] - mt[nb][j]);
+            const float p = exp2_ftz(sc[nb][u][2 * r + j] - mt[nb][j]);
             l[nb][j] += p;
             zs[nb][j] = fmaf(p, vc, zs[nb][j]);
             w2[j] = p * vs;
@@ -454,7 +446,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
         }
       }
       // V: keys of rows 2 lc, 2 lc + 1 (+ 8), word lr (half a word for 32 elements).
-      uint32_t x[2][4];
+      uint32_t x[2][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int word = DH == 64 ? lr : lr >> 1;
@@ -483,106 +475,242 @@ __global__ void __launch_bounds__(kAttnThreads, 2) kv4_attn_kernel(AttnArgs a) {
       for (int nb = 0; nb < NB; ++nb)
         mma_bf16(ones[nb], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, pw[nb][0], pw[nb][1]);
     }
-    __syncwarp();
-    if (lane == 0 && i + kStages < mine) issue(i + kStages);
   }
 
-  // This warp's state per head: output (lane lr holds dims DH/8 lr ...), max, sum.
-  __syncthreads();  // every warp is done with the ring
-  float* st = reinterpret_cast<float*>(sm);
+  // The unit's outputs (whole), or this warp's part of them into `slot`.
+  __device__ __forceinline__ void finish(const AttnArgs& a, int b, int g, bool whole, long long slot) {
+    const int H = heads_of_group(a, g);
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int j = 0; j < HPL; ++j) {
-      const int h = HPL == 1 ? lc : nb * 8 + 2 * lc + j;
-      float ls = l[nb][j], z = zs[nb][j];
+      for (int j = 0; j < HPL; ++j) {
+        const int h = HPL == 1 ? lc : nb * 8 + 2 * lc + j;
+        float ls = l[nb][j], z = zs[nb][j];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        ls += __shfl_xor_sync(0xffffffffu, ls, o);
-        z += __shfl_xor_sync(0xffffffffu, z, o);
+        for (int o = 4; o < 32; o <<= 1) {
+          ls += __shfl_xor_sync(0xffffffffu, ls, o);
+          z += __shfl_xor_sync(0xffffffffu, z, o);
+        }
+        if (h >= H) continue;
+        z = fmaf(-136.0f, ones[nb][j], z);
+        const float f = whole ? 1.0f / ls : 1.0f;
+        float o[DH / 8];  // elements DH/8 lr ...
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          o[2 * t] = (acc[nb][t][j] + z) * f;
+          o[2 * t + 1] = (acc[nb][t][j + 2] + z) * f;
+        }
+        if (whole) {
+          uint32_t* d = reinterpret_cast<uint32_t*>(out_row(a, b, g, h, DH) + lr * (DH / 8));
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i) d[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+        } else {
+          float4* d = reinterpret_cast<float4*>(a.part_o + (slot * a.H + h) * DH + lr * (DH / 8));
+#pragma unroll
+          for (int i = 0; i < DH / 32; ++i) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          if (lr == 0) a.part_ml[slot * a.H + h] = make_float2(m[nb][j], ls);
+        }
       }
-      if (h >= H) continue;
-      float* d = st + (warp * a.H + h) * S::STATE;
-      z = fmaf(-136.0f, ones[nb][j], z);
+  }
+};
+
+template <int DH, int HPL, int NB>
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(AttnArgs a) {
+  using S = AttnShape<DH>;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ long long before[kAttnThreads + 1];  // tiles before each thread's run of sequences
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + static_cast<size_t>(kAttnWarps) * S::RING);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kAttnWarps * kStages);
+  if (tid < kAttnWarps * kStages) mbar_init(bars + tid, 1u);
+  if (tid == 0) *abort_flag = 0;
+  fence_barrier_init();
+  pdl_wait();  // q, lens and the newest rows come from earlier kernels
+  pdl_launch_dependents();
+  // Tiles of all sequences before each run of `run` of them.
+  const int run = (a.B + kAttnThreads - 1) / kAttnThreads;
+  {
+    long long s = 0;
+    for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) s += static_cast<long long>(tiles_of(keys_of(a, b))) * a.G;
+    long long in = s;  // inclusive over the warp
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        d[lr * (DH / 8) + 2 * t] = acc[nb][t][j] + z;
-        d[lr * (DH / 8) + 2 * t + 1] = acc[nb][t][j + 2] + z;
-      }
-      if (lr == 0) {
-        d[DH] = m[nb][j];
-        d[DH + 1] = ls;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += v;
     }
-  __syncthreads();
-  const bool whole = n <= a.span;
-  for (int i = tid; i < H * DH; i += kAttnThreads) {
-    const int h = i / DH, d = i % DH;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) mx = fmaxf(mx, st[(w * a.H + h) * S::STATE + DH]);
-    const float mu = mx == -INFINITY ? 0.0f : mx;
-    float o = 0.0f, ls = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      const float* s = st + (w * a.H + h) * S::STATE;
-      const float f = exp2f(s[DH] - mu);
-      o = fmaf(f, s[d], o);
-      ls = fmaf(f, s[DH + 1], ls);
+    before[tid + 1] = in;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+    long long base = 0;
+    for (int w = 0; w < warp; ++w) base += before[32 * (w + 1)];
+    __syncthreads();
+    before[tid + 1] = in + base;
+    __syncthreads();
+  }
+  // Warps of all CTAs, first every CTA's warp 0: short work spreads over the SMs.
+  const long long W = static_cast<long long>(gridDim.x) * kAttnWarps, gw = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
+  const long long total = before[kAttnThreads], share = max((total + W - 1) / W, 1ll);
+  if (blockIdx.x == 0) {  // for the join
+    long long s = before[tid];
+    for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
+      a.starts[b] = s;
+      s += static_cast<long long>(tiles_of(keys_of(a, b))) * a.G;
     }
-    if (whole) {
-      store_out(a, b, g, h, d, DH, o / ls);
+    if (tid == 0) a.starts[a.B] = share;
+  }
+  // Sequences without keys: zeros.
+  const long long units = static_cast<long long>(a.B) * a.G;
+  for (long long u = gw * 32 + lane; u < units; u += W * 32) {
+    const int b = static_cast<int>(u / a.G), g = static_cast<int>(u - static_cast<long long>(b) * a.G);
+    if (keys_of(a, b) == 0)
+      for (int h = 0; h < heads_of_group(a, g); ++h)
+        for (int i = 0; i < DH / 8; ++i) reinterpret_cast<uint4*>(out_row(a, b, g, h, DH))[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const long long w0 = gw * share, w1 = min(total, w0 + share);
+  if (w0 >= w1) return;
+  // The share's first tile: the run of sequences, then the sequence.
+  Cursor rd;
+  {
+    int lo = 0, hi = kAttnThreads;  // the last entry of `before` that is <= w0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (before[mid] <= w0) lo = mid;
+      else hi = mid;
+    }
+    long long s = before[lo];
+    rd.b = lo * run;
+    for (;; ++rd.b) {
+      rd.n = keys_of(a, rd.b);
+      const long long t = static_cast<long long>(tiles_of(rd.n)) * a.G;
+      if (w0 < s + t) break;
+      s += t;
+    }
+    const int tb = tiles_of(rd.n), at = static_cast<int>(w0 - s);
+    rd.g = at / tb;
+    rd.t = at - rd.g * tb;
+  }
+  const int count = static_cast<int>(w1 - w0);
+  uint8_t* ring = sm + warp * S::RING;
+  uint64_t* full = bars + warp * kStages;
+  Cursor wr = rd;
+  // Tile wr into stage i: its keys, rounded up to an even count (16-byte
+  // pieces; the capacity is a multiple of 16).
+  auto issue = [&](int i) {
+    const int nk = (min(kTile, wr.n - wr.t * kTile) + 1) & ~1;
+    const long long row = (static_cast<long long>(wr.b) * a.G + wr.g) * a.c.capacity + wr.t * kTile;
+    uint8_t* s = ring + i * S::TILE_BYTES;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full + i, static_cast<uint32_t>(nk) * (2 * S::ROW + 8));
+      bulk_load(s, a.c.k_codes + row * S::ROW, nk * S::ROW, full + i);
+      bulk_load(s + kTile * 2 * S::ROW, a.c.meta + row * 4, nk * 8, full + i);
+      bulk_load(s + kTile * S::ROW, a.c.v_codes + row * S::ROW, nk * S::ROW, full + i);
+    }
+  };
+  int issued = 0;
+  for (; issued < min(count, kStages); ++issued) {
+    if (issued > 0) wr.next(a);
+    issue(issued);
+  }
+  Warp<DH, HPL, NB> w;
+  w.lr = lane >> 2;
+  w.lc = lane & 3;
+  int first = rd.t;  // of the unit in this share
+  w.start(a, rd.b, rd.g);
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, phase, abort_flag))) break;
+    const int left = rd.n - rd.t * kTile;
+    const uint8_t* s = ring + stage * S::TILE_BYTES;
+    if (left >= kTile) w.template tile<true>(s, left);
+    else w.template tile<false>(s, left);
+    __syncwarp();
+    if (issued < count) {
+      wr.next(a);
+      issue(stage);
+      ++issued;
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    const bool end = left <= kTile;
+    if (end || i + 1 == count) {
+      w.finish(a, rd.b, rd.g, first == 0 && end, gw + static_cast<long long>(rd.b) * a.G + rd.g);
+      if (i + 1 == count) break;
+      rd.next(a);
+      first = 0;
+      w.start(a, rd.b, rd.g);
     } else {
-      const long long at = ((static_cast<long long>(b) * a.G + g) * a.spans + span) * a.H + h;
-      a.part_o[at * DH + d] = o;
-      if (d == 0) a.part_ml[at] = make_float2(mx, ls);
+      ++rd.t;
     }
   }
 }
 
-// Joins the spans of the sequences that have several: one CTA per (sequence,
-// group), one thread per (head, element).
+// Joins the parts of the units that lie in several shares: one CTA per unit,
+// H DH threads per part, as many parts at a time as the CTA has room for.
+constexpr int kJoinThreads = 512;
 template <int DH>
-__global__ void __launch_bounds__(1024) kv4_merge_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(1024) kv4_join_kernel(AttnArgs a) {
+  extern __shared__ float jm[];  // [rows][H DH + 2 H]
   pdl_wait();
   pdl_launch_dependents();
   const int g = blockIdx.x % a.G, b = blockIdx.x / a.G;
-  const int h = threadIdx.x / DH, d = threadIdx.x % DH;
-  const int n = keys_of(a, b);
-  if (n <= a.span || h >= heads_of_group(a, g)) return;
-  const int spans = (n + a.span - 1) / a.span;
-  const long long at0 = (static_cast<long long>(b) * a.G + g) * a.spans;
+  const int tb = tiles_of(keys_of(a, b));
+  if (tb == 0) return;
+  const long long share = a.starts[a.B], s0 = a.starts[b] + static_cast<long long>(g) * tb;
+  const long long p0 = s0 / share, p1 = (s0 + tb - 1) / share;  // the warps of its tiles
+  if (p0 == p1) return;
+  const int HD = a.H * DH, row = threadIdx.x / HD, rows = blockDim.x / HD, i = threadIdx.x % HD, h = i / DH;
+  const long long slot0 = p0 + blockIdx.x;
+  const int parts = static_cast<int>(p1 - p0 + 1);
+  const bool on = h < heads_of_group(a, g);
   float m = -INFINITY;
-#pragma unroll 8
-  for (int c = 0; c < spans; ++c) m = fmaxf(m, a.part_ml[(at0 + c) * a.H + h].x);
+  if (on)
+#pragma unroll 4
+    for (int c = row; c < parts; c += rows) m = fmaxf(m, a.part_ml[(slot0 + c) * a.H + h].x);
   const float mu = m == -INFINITY ? 0.0f : m;
   float o = 0.0f, l = 0.0f;
-#pragma unroll 8
-  for (int c = 0; c < spans; ++c) {
-    const float2 ml = a.part_ml[(at0 + c) * a.H + h];
-    const float w = exp2f(ml.x - mu);
-    l = fmaf(w, ml.y, l);
-    o = fmaf(w, a.part_o[((at0 + c) * a.H + h) * DH + d], o);
+  if (on)
+#pragma unroll 4
+    for (int c = row; c < parts; c += rows) {
+      const float2 ml = a.part_ml[(slot0 + c) * a.H + h];
+      const float w = exp2_ftz(ml.x - mu);
+      l = fmaf(w, ml.y, l);
+      o = fmaf(w, a.part_o[(slot0 + c) * HD + i], o);
+    }
+  float* mine = jm + row * 3 * HD;
+  mine[i] = o;
+  mine[HD + i] = l;
+  mine[2 * HD + i] = m;
+  __syncthreads();
+  if (row != 0 || !on) return;
+  float mx = m;
+  for (int r = 1; r < rows; ++r) mx = fmaxf(mx, jm[(r * 3 + 2) * HD + i]);
+  const float mxu = mx == -INFINITY ? 0.0f : mx;
+  o = l = 0.0f;
+  for (int r = 0; r < rows; ++r) {
+    const float w = exp2_ftz(jm[(r * 3 + 2) * HD + i] - mxu);
+    l = fmaf(w, jm[(r * 3 + 1) * HD + i], l);
+    o = fmaf(w, jm[r * 3 * HD + i], o);
   }
-  store_out(a, b, g, h, d, DH, o / l);
+  out_row(a, b, g, h, DH)[i % DH] = __bfloat16_as_ushort(__float2bfloat16_rn(o / l));
 }
 
-// Spans per (sequence, group): enough CTAs for kAttnCtas, each with at least
-// one tile per warp.
-constexpr int kAttnCtas = 148 * 2 * 8;
-int attn_spans(int B, int G, int T) {
-  const long long units = static_cast<long long>(B) * G, most = (T + kMinSpan - 1) / kMinSpan;
-  const long long want = (kAttnCtas + units - 1) / units;
-  return static_cast<int>(want < most ? want : most);
+int attn_ctas(int B, int G, int T) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const long long most = static_cast<long long>(sms < 148 ? sms : 148) * kAttnCtasPerSm,
+                  tiles = static_cast<long long>(B) * G * ((T + kTile - 1) / kTile);
+  return static_cast<int>(tiles < most ? tiles : most);
 }
 
 template <int DH, int HPL, int NB>
 int launch_attn(const AttnArgs& a, void* stream) {
-  const size_t smem = AttnShape<DH>::smem(a.H);
-  const int e = ensure_smem<kv4_attn_kernel<DH, HPL, NB>>(static_cast<int>(smem));
+  const int e = ensure_smem<kv4_attn_kernel<DH, HPL, NB>>(static_cast<int>(AttnShape<DH>::smem()));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_attn_kernel<DH, HPL, NB>, dim3(a.spans, static_cast<unsigned>(a.B) * a.G), dim3(kAttnThreads),
-                    smem, stream, a);
+  return launch_pdl(kv4_attn_kernel<DH, HPL, NB>, dim3(attn_ctas(a.B, a.G, a.T)), dim3(kAttnThreads),
+                    AttnShape<DH>::smem(), stream, a);
 }
 
 template <int DH>
@@ -590,8 +718,23 @@ int attention(const AttnArgs& a, void* stream) {
   const int e = a.H <= 4 ? launch_attn<DH, 1, 1>(a, stream)
                 : a.H <= 8 ? launch_attn<DH, 2, 1>(a, stream)
                            : launch_attn<DH, 2, 2>(a, stream);
-  if (e != cudaSuccess || a.spans == 1) return e;
-  return launch_pdl(kv4_merge_kernel<DH>, dim3(static_cast<unsigned>(a.B) * a.G), dim3(a.H * DH), 0, stream, a);
+  if (e != cudaSuccess || a.T <= kTile) return e;  // one tile per unit: nothing to join
+  const int HD = a.H * DH, rows = HD >= kJoinThreads ? 1 : kJoinThreads / HD;
+  return launch_pdl(kv4_join_kernel<DH>, dim3(static_cast<unsigned>(a.B) * a.G), dim3(rows * HD),
+                    static_cast<size_t>(rows) * 3 * HD * 4, stream, a);
+}
+
+// Workspace: the parts' slots, then the sequences' starts.
+struct AttnWs {
+  size_t ml, starts, total;
+};
+AttnWs attn_ws(int B, int G, int H, int dh) {
+  const size_t slots = static_cast<size_t>(B) * G + kMaxAttnWarps;
+  AttnWs w;
+  w.ml = (slots * H * dh * 4 + 255) / 256 * 256;
+  w.starts = (w.ml + slots * H * 8 + 255) / 256 * 256;
+  w.total = w.starts + (static_cast<size_t>(B) + 1) * 8;
+  return w;
 }
 
 unsigned store_ctas(int B, int G, int T, int dh) {
@@ -618,10 +761,7 @@ int kv4_read(int B, int G, int T, int dh, const gqe_kv4& cache, const int32_t* s
                   : launch_pdl(read_kernel<32>, grid, dim3(kv4_impl::kThreads), 0, stream, a);
 }
 
-size_t kv4_attention_ws_bytes(int B, int G, int T, int H, int dh) {
-  const size_t units = static_cast<size_t>(B) * G * attn_spans(B, G, T) * H;
-  return (units * dh * 4 + 255) / 256 * 256 + units * 8;
-}
+size_t kv4_attention_ws_bytes(int B, int G, int H, int dh) { return attn_ws(B, G, H, dh).total; }
 
 int kv4_attention(int B, int G, int T, int k, int dh, const uint16_t* Q, const uint16_t* Qs, const gqe_kv4& cache,
                   const int32_t* lens, int len_add, uint16_t* out, int ldo, void* ws, void* stream) {
@@ -636,12 +776,10 @@ int kv4_attention(int B, int G, int T, int k, int dh, const uint16_t* Q, const u
   a.T = T;
   a.k = k;
   a.H = k + (Qs != nullptr ? 1 : 0);
-  const int spans = attn_spans(B, G, T);
-  a.span = ((T + spans - 1) / spans + kTile - 1) / kTile * kTile;
-  a.spans = (T + a.span - 1) / a.span;
-  const size_t units = static_cast<size_t>(B) * G * a.spans * a.H;
+  const AttnWs w = attn_ws(B, G, a.H, dh);
   a.part_o = static_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + (units * dh * 4 + 255) / 256 * 256);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.ml);
+  a.starts = reinterpret_cast<long long*>(static_cast<char*>(ws) + w.starts);
   a.out = out;
   a.ldo = ldo;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(dh)));

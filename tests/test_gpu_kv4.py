@@ -143,6 +143,9 @@ ATTN = {
     "over_and_under": (4, 2, 1, True, 64, 100, [-5, 400, 100, 2 ** 31 - 1]),
     "spans": (2, 4, 2, True, 64, 9001, [9001, 4095]),
     "many_sequences": (150, 8, 1, True, 64, 70, None),
+    "wide_batch": (700, 2, 1, True, 32, 200, [(37 * b) % 201 if b % 3 else 0 for b in range(700)]),
+    "one_live_sequence": (300, 1, 2, False, 64, 3000, [0] * 299 + [3000]),
+    "nothing_live": (5, 2, 1, True, 64, 50, [0, -1, 0, -7, 0]),
 }
 
 
