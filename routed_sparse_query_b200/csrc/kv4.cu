@@ -164,16 +164,21 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    the same rounded weights (a product with ones); the rest, sum p (zero_v
 //    + 8 scale_v), is kept in fp32. The rounding of p thus meets codes around
 //    zero, |n - 8| <= 8.
-//  - Heads sit in the even columns (up to 4 heads per group; else in all):
-//    the scores' accumulator then holds one head per lane, and what the
-//    softmax does per key is done once per lane and not twice.
+//  - Up to 4 heads per group: the heads sit in the even columns, 4 / HP times
+//    over (HP = 1, 2 or 4 >= the group's heads), so the scores' accumulator
+//    holds one head per lane and every copy of the column can take other keys:
+//    lane column lc forms the weights of head lc % HP for the 16-key blocks
+//    u = lc / HP (mod 4 / HP) only, and leaves 0 in the others. The copies'
+//    sums are added at the end of a unit. Without that one head's softmax
+//    costs what four heads' does (measured at 64 x 32k, one head in 7 of 8
+//    groups: see kv4_attn_kernel).
 //  - A transposed 8 x 8 move turns the weights from (key, head) to the second
 //    product's (head, keys) order.
 // The work is cut over warps: the tiles of 64 keys of all (sequence, group)
 // units, laid end to end, are dealt in equal contiguous shares, so that ragged
 // lengths, few long sequences and many short ones all fill the SMs alike. A
-// warp streams its tiles by bulk copies through a ring of its own, across the
-// units' borders, with its own running maximum and no CTA-wide barrier in the
+// warp streams its tiles (cp.async: a bulk copy per array and tile cost more
+// instructions than its nine 512-byte pieces) through a ring of its own, across the units' borders, with its own running maximum and no CTA-wide barrier in the
 // loop. A unit that lies in one warp's share is written out by it; the parts
 // of the others are joined by a second kernel.
 constexpr int kAttnWarps = 8;
@@ -219,6 +224,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A B.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -240,34 +253,48 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// Row r of a 16-key block holds key row_key(r): the order that keeps both the
-// K reads (rows 0..3 and 4..7 together) and the V reads (even rows, odd rows
-// together) on distinct banks (keys distinct mod 4).
-__device__ __forceinline__ int row_key(int r) { return (0x57463120u >> (4 * (r & 7)) & 7) + (r & 8); }
+// Four 8 x 8 blocks of 16-bit elements, each read by rows (lane 8 i + j: row j
+// of block i) and handed out by columns: lane (lr, lc) gets elements 2 lc and
+// 2 lc + 1 of column lr of each.
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void load_transposed(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(addr)
+               : "memory");
+}
 
 template <int DH>
 struct AttnShape {
   static constexpr int ROW = DH / 2;                       // bytes of a row's codes
   static constexpr int TILE_BYTES = kTile * (2 * ROW + 8);  // K, V, meta
   static constexpr int RING = kStages * TILE_BYTES;
-  static constexpr size_t smem() { return static_cast<size_t>(kAttnWarps) * (RING + kStages * 8) + 16; }
+  static constexpr size_t smem() { return static_cast<size_t>(kAttnWarps) * RING; }
 };
 
-// A place in the units' tiles.
+// A place in the units' tiles: a unit and the keys from the place to its end.
 struct Cursor {
-  int b, g, t, n;  // sequence, group, tile of the unit, keys of the sequence
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    if (++t < tiles_of(n)) return;
-    t = 0;
-    if (++g < a.G) return;
-    g = 0;
-    do ++b;
-    while (b < a.B && (n = keys_of(a, b)) == 0);
+  int b, g, left;
+  __device__ __forceinline__ long long row(const AttnArgs& a) const {  // cache row of the place
+    return (static_cast<long long>(b) * a.G + g) * a.c.capacity + (keys_of(a, b) - left);
+  }
+  __device__ __forceinline__ void next_unit(const AttnArgs& a) {
+    if (++g == a.G) {
+      g = 0;
+      do ++b;
+      while (b < a.B && keys_of(a, b) == 0);
+    }
+    left = b < a.B ? keys_of(a, b) : 0;
   }
 };
 
 // HPL: heads per lane (1: even columns, at most 4 heads; 2: all columns);
-// NB: column blocks of 8 (2 only with HPL = 2).
+// NB: column blocks of 8 (2 only with HPL = 2). HP of the members: see above (4 with HPL = 2).
 template <int DH, int HPL, int NB>
 struct Warp {
   using S = AttnShape<DH>;
@@ -279,11 +306,11 @@ struct Warp {
   float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4], ones[NB][4];
   int lr, lc;
 
-  __device__ __forceinline__ void start(const AttnArgs& a, int b, int g) {
+  __device__ __forceinline__ void start(const AttnArgs& a, int b, int g, int hp) {
     const int H = heads_of_group(a, g);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int h = HPL == 1 ? ((lr & 1) ? H : lr >> 1) : nb * 8 + lr;
+      const int h = HPL == 1 ? ((lr & 1) ? H : (lr >> 1) & (hp - 1)) : nb * 8 + lr;
       // Lane (lr, lc) holds words 2 lc, 2 lc + 1 of a 64-element row, word lc of a 32-element one.
       float v[DH / 4], mx = 0.0f, sum = 0.0f;
 #pragma unroll
@@ -338,18 +365,22 @@ struct Warp {
   }
 
   // One tile in shared memory; FULL: 64 keys, else the first `left`.
-  template <bool FULL>
+  template <int HP, bool FULL>
   __device__ __forceinline__ void tile(const uint8_t* tk, int left) {
-    const uint8_t* tv = tk + kTile * S::ROW;
-    const uint8_t* tm = tv + kTile * S::ROW;
-    const int kr = row_key(lr), v0 = row_key(2 * lc), v1 = row_key(2 * lc + 1);
+    constexpr int R = 4 / HP;   // copies of a head's column
+    constexpr int OWN = SUB / R;  // 16-key blocks whose weights a lane forms: part + R i
+    const int part = lc / HP;
+    const uint8_t* tm = tk + 2 * kTile * S::ROW;
+    // This lane's row of the V blocks: 8-key half (lane / 8) % 2, 16-byte piece (lane / 16) of it.
+    const int lane = 4 * lr + lc;
+    const uint32_t tva = smem_u32(tk) + kTile * S::ROW + (lane & 15) * S::ROW + (DH == 64 ? lane & 16 : 0);
     float sc[NB][SUB][4];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      uint32_t w[2][DH / 32];  // rows kr, kr + 8
+      uint32_t w[2][DH / 32];  // rows lr, lr + 8
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const uint8_t* p = tk + (16 * u + kr + 8 * r) * S::ROW + lc * (S::ROW / 4);
+        const uint8_t* p = tk + (16 * u + lr + 8 * r) * S::ROW + lc * (S::ROW / 4);
         if constexpr (DH == 64) {
           const uint2 x = *reinterpret_cast<const uint2*>(p);
           w[r][0] = x.x;
@@ -359,41 +390,42 @@ struct Warp {
         }
       }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nb][u][x] = 0.0f;
-#pragma unroll
       for (int s = 0; s < KS; ++s) {
         const uint32_t x0 = s & 1 ? w[0][s / 2] >> 8 : w[0][s / 2], x1 = s & 1 ? w[1][s / 2] >> 8 : w[1][s / 2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          mma_f16(sc[nb][u], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[nb][s][0],
-                  qf[nb][s][1]);
+        for (int nb = 0; nb < NB; ++nb) {
+          const uint32_t f0 = x0 & 0x000f000fu, f1 = x1 & 0x000f000fu, f2 = x0 & 0x00f000f0u, f3 = x1 & 0x00f000f0u;
+          if (s == 0) mma_f16_first(sc[nb][u], f0, f1, f2, f3, qf[nb][s][0], qf[nb][s][1]);
+          else mma_f16(sc[nb][u], f0, f1, f2, f3, qf[nb][s][0], qf[nb][s][1]);
+        }
       }
     }
-    // Scores, then the tile's maximum per head.
-    float mt[NB][HPL];
+    // Scores of this lane's blocks, then the tile's maximum per head.
+    float mt[NB][HPL], ps[NB][HPL][OWN][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < HPL; ++j) mt[nb][j] = -INFINITY;
-    uint32_t mv[SUB][2];  // the values' (scale, zero)
+    uint32_t mv[OWN][2];  // the values' (scale, zero)
 #pragma unroll
-    for (int u = 0; u < SUB; ++u)
+    for (int i = 0; i < OWN; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int key = 16 * u + kr + 8 * r;
+        const int key = 16 * (part + R * i) + lr + 8 * r;
         const uint2 mm = *reinterpret_cast<const uint2*>(tm + key * 8);
         const bool on = FULL || key < left;
         const float ks = bf16_f(mm.x & 0xffffu), kz = __uint_as_float(mm.x & 0xffff0000u);
-        mv[u][r] = on ? mm.y : 0u;
+        mv[i][r] = on ? mm.y : 0u;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < HPL; ++j) {
-            float& s = sc[nb][u][2 * r + j];
-            s = on ? fmaf(s * fac[nb][j], ks, kz * qsum[nb][j]) : -INFINITY;
-            mt[nb][j] = fmaxf(mt[nb][j], s);
+            float d = sc[nb][R * i][2 * r + j];
+#pragma unroll
+            for (int q = 1; q < R; ++q) d = part == q ? sc[nb][R * i + q][2 * r + j] : d;
+            const float v = on ? fmaf(d * fac[nb][j], ks, kz * qsum[nb][j]) : -INFINITY;
+            ps[nb][j][i][r] = v;
+            mt[nb][j] = fmaxf(mt[nb][j], v);
           }
       }
     bool grown = false;
@@ -403,7 +435,7 @@ struct Warp {
 #pragma unroll
       for (int j = 0; j < HPL; ++j) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mt[nb][j] = fmaxf(mt[nb][j], __shfl_xor_sync(0xffffffffu, mt[nb][j], o));
+        for (int o = HP; o < 32; o <<= 1) mt[nb][j] = fmaxf(mt[nb][j], __shfl_xor_sync(0xffffffffu, mt[nb][j], o));
         const float mn = fmaxf(m[nb][j], mt[nb][j]);
         grown = grown || mn > m[nb][j];
         al[nb][j] = m[nb][j] == mn ? 1.0f : exp2_ftz(m[nb][j] - mn);
@@ -426,47 +458,45 @@ struct Warp {
           }
         }
     }
+    // Weights p scale_v of this lane's blocks, packed as (column 2 lc, 2 lc + 1).
+    uint32_t pk[NB][OWN][2];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      uint32_t pw[NB][2];
+    for (int i = 0; i < OWN; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float vs = bf16_f(mv[u][r] & 0xffffu), vc = fmaf(8.0f, vs, __uint_as_float(mv[u][r] & 0xffff0000u));
+        const float vs = bf16_f(mv[i][r] & 0xffffu), vc = fmaf(8.0f, vs, __uint_as_float(mv[i][r] & 0xffff0000u));
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float w2[2] = {0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < HPL; ++j) {
-            const float p = exp2_ftz(sc[nb][u][2 * r + j] - mt[nb][j]);
+            const float p = exp2_ftz(ps[nb][j][i][r] - mt[nb][j]);
             l[nb][j] += p;
             zs[nb][j] = fmaf(p, vc, zs[nb][j]);
             w2[j] = p * vs;
           }
-          pw[nb][r] = transpose8(pack_bf16x2(w2[0], w2[1]));
+          pk[nb][i][r] = pack_bf16x2(w2[0], w2[1]);
         }
       }
-      // V: keys of rows 2 lc, 2 lc + 1 (+ 8), word lr (half a word for 32 elements).
-      uint32_t x[2][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int word = DH == 64 ? lr : lr >> 1;
-        const uint32_t a0 = *reinterpret_cast<const uint32_t*>(tv + (16 * u + v0 + 8 * r) * S::ROW + word * 4);
-        const uint32_t a1 = *reinterpret_cast<const uint32_t*>(tv + (16 * u + v1 + 8 * r) * S::ROW + word * 4);
-        if constexpr (DH == 64) {
-          x[r][0] = __byte_perm(a0, a1, 0x5410);
-          x[r][1] = __byte_perm(a0, a1, 0x7632);
-        } else {
-          x[r][0] = __byte_perm(a0, a1, lr & 1 ? 0x7632 : 0x5410);
-        }
-      }
+    for (int u = 0; u < SUB; ++u) {
+      uint32_t pw[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) pw[nb][r] = transpose8(R == 1 || part == u % R ? pk[nb][u / R][r] : 0u);
+      // V: 16-bit column lr (4 codes) of keys 2 lc, 2 lc + 1 (+ 8), for each
+      // 32 elements of a row: element 32 x + 4 lr + nibble.
+      uint32_t x[2 * (DH / 32)];  // [32 elements][keys + 8 r]
+      load_transposed(x, tva + 16 * u * S::ROW);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const int hw = t / 2, sh = 8 * (t & 1);
         uint32_t f[4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          f[2 * r] = ((x[r][hw] >> sh) & 0x000f000fu) | 0x43004300u;
-          f[2 * r + 1] = ((x[r][hw] >> (sh + 4)) & 0x000f000fu) | 0x43004300u;
+          f[2 * r] = ((x[2 * hw + r] >> sh) & 0x000f000fu) | 0x43004300u;
+          f[2 * r + 1] = ((x[2 * hw + r] >> (sh + 4)) & 0x000f000fu) | 0x43004300u;
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) mma_bf16(acc[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
@@ -478,36 +508,50 @@ struct Warp {
   }
 
   // The unit's outputs (whole), or this warp's part of them into `slot`.
-  __device__ __forceinline__ void finish(const AttnArgs& a, int b, int g, bool whole, long long slot) {
+  __device__ __forceinline__ void finish(const AttnArgs& a, int b, int g, int hp, bool whole, long long slot) {
     const int H = heads_of_group(a, g);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < HPL; ++j) {
-        const int h = HPL == 1 ? lc : nb * 8 + 2 * lc + j;
+        const int h = HPL == 1 ? lc : nb * 8 + 2 * lc + j;  // copies: h >= hp
         float ls = l[nb][j], z = zs[nb][j];
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {  // the copies of the head's column
+          if (o < hp) continue;
+          ls += __shfl_xor_sync(0xffffffffu, ls, o);
+          z += __shfl_xor_sync(0xffffffffu, z, o);
+          ones[nb][j] += __shfl_xor_sync(0xffffffffu, ones[nb][j], o);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            acc[nb][t][j] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j], o);
+            acc[nb][t][j + 2] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j + 2], o);
+          }
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           ls += __shfl_xor_sync(0xffffffffu, ls, o);
           z += __shfl_xor_sync(0xffffffffu, z, o);
         }
-        if (h >= H) continue;
+        if (h >= H || (HPL == 1 && h >= hp)) continue;
         z = fmaf(-136.0f, ones[nb][j], z);
         const float f = whole ? 1.0f / ls : 1.0f;
-        float o[DH / 8];  // elements DH/8 lr ...
+        float o[DH / 8];  // elements 32 x + 4 lr + {0..3}, x < DH / 32
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           o[2 * t] = (acc[nb][t][j] + z) * f;
           o[2 * t + 1] = (acc[nb][t][j + 2] + z) * f;
         }
         if (whole) {
-          uint32_t* d = reinterpret_cast<uint32_t*>(out_row(a, b, g, h, DH) + lr * (DH / 8));
+          uint16_t* d = out_row(a, b, g, h, DH) + 4 * lr;
 #pragma unroll
-          for (int i = 0; i < DH / 16; ++i) d[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+          for (int i = 0; i < DH / 32; ++i)
+            *reinterpret_cast<uint2*>(d + 32 * i) = make_uint2(pack_bf16x2(o[4 * i], o[4 * i + 1]), pack_bf16x2(o[4 * i + 2], o[4 * i + 3]));
         } else {
-          float4* d = reinterpret_cast<float4*>(a.part_o + (slot * a.H + h) * DH + lr * (DH / 8));
+          float* d = a.part_o + (slot * a.H + h) * DH + 4 * lr;
 #pragma unroll
-          for (int i = 0; i < DH / 32; ++i) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < DH / 32; ++i)
+            *reinterpret_cast<float4*>(d + 32 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           if (lr == 0) a.part_ml[slot * a.H + h] = make_float2(m[nb][j], ls);
         }
       }
@@ -520,11 +564,6 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ long long before[kAttnThreads + 1];  // tiles before each thread's run of sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + static_cast<size_t>(kAttnWarps) * S::RING);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kAttnWarps * kStages);
-  if (tid < kAttnWarps * kStages) mbar_init(bars + tid, 1u);
-  if (tid == 0) *abort_flag = 0;
-  fence_barrier_init();
   pdl_wait();  // q, lens and the newest rows come from earlier kernels
   pdl_launch_dependents();
   // Tiles of all sequences before each run of `run` of them.
@@ -570,6 +609,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   if (w0 >= w1) return;
   // The share's first tile: the run of sequences, then the sequence.
   Cursor rd;
+  bool first_whole;  // the share holds the unit's first tile
   {
     int lo = 0, hi = kAttnThreads;  // the last entry of `before` that is <= w0
     while (hi - lo > 1) {
@@ -579,70 +619,103 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
     }
     long long s = before[lo];
     rd.b = lo * run;
+    int n;
     for (;; ++rd.b) {
-      rd.n = keys_of(a, rd.b);
-      const long long t = static_cast<long long>(tiles_of(rd.n)) * a.G;
+      n = keys_of(a, rd.b);
+      const long long t = static_cast<long long>(tiles_of(n)) * a.G;
       if (w0 < s + t) break;
       s += t;
     }
-    const int tb = tiles_of(rd.n), at = static_cast<int>(w0 - s);
+    const int tb = tiles_of(n), at = static_cast<int>(w0 - s);
     rd.g = at / tb;
-    rd.t = at - rd.g * tb;
+    rd.left = n - (at - rd.g * tb) * kTile;
+    first_whole = rd.left == n;
   }
   const int count = static_cast<int>(w1 - w0);
-  uint8_t* ring = sm + warp * S::RING;
-  uint64_t* full = bars + warp * kStages;
+  const uint32_t ring = smem_u32(sm) + warp * S::RING;
+  // Loads: the next tile's place, and this lane's pointers at its cache row.
   Cursor wr = rd;
-  // Tile wr into stage i: its keys, rounded up to an even count (16-byte
-  // pieces; the capacity is a multiple of 16).
+  const uint8_t *pk, *pv, *pm;
+  auto seek = [&] {
+    const long long row = wr.row(a);
+    pk = a.c.k_codes + row * S::ROW + lane * 16;
+    pv = a.c.v_codes + row * S::ROW + lane * 16;
+    pm = reinterpret_cast<const uint8_t*>(a.c.meta) + row * 8 + lane * 16;
+  };
   auto issue = [&](int i) {
-    const int nk = (min(kTile, wr.n - wr.t * kTile) + 1) & ~1;
-    const long long row = (static_cast<long long>(wr.b) * a.G + wr.g) * a.c.capacity + wr.t * kTile;
-    uint8_t* s = ring + i * S::TILE_BYTES;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(full + i, static_cast<uint32_t>(nk) * (2 * S::ROW + 8));
-      bulk_load(s, a.c.k_codes + row * S::ROW, nk * S::ROW, full + i);
-      bulk_load(s + kTile * 2 * S::ROW, a.c.meta + row * 4, nk * 8, full + i);
-      bulk_load(s + kTile * S::ROW, a.c.v_codes + row * S::ROW, nk * S::ROW, full + i);
+    constexpr int CP = kTile * S::ROW / 512;  // 16-byte pieces of K (or V) per lane
+    const uint32_t d = ring + i * S::TILE_BYTES + lane * 16;
+    if (wr.left >= kTile) {
+#pragma unroll
+      for (int j = 0; j < CP; ++j) cp_async_16(d + 512 * j, pk + 512 * j, 16);
+      cp_async_16(d + 2 * kTile * S::ROW, pm, 16);
+#pragma unroll
+      for (int j = 0; j < CP; ++j) cp_async_16(d + kTile * S::ROW + 512 * j, pv + 512 * j, 16);
+    } else {
+      // The sequence's last tile: what lies behind it (and perhaps behind the
+      // buffer) is not read, its place is filled with zeros.
+#pragma unroll
+      for (int j = 0; j < CP; ++j) {
+        const bool on = 16 * (lane + 32 * j) < wr.left * S::ROW;
+        cp_async_16(d + 512 * j, on ? pk + 512 * j : a.c.k_codes, on ? 16 : 0);
+        cp_async_16(d + kTile * S::ROW + 512 * j, on ? pv + 512 * j : a.c.v_codes, on ? 16 : 0);
+      }
+      const bool on = 2 * lane < wr.left;  // two keys per piece (the capacity is even)
+      cp_async_16(d + 2 * kTile * S::ROW, on ? pm : reinterpret_cast<const uint8_t*>(a.c.meta), on ? 16 : 0);
+    }
+    pk += kTile * S::ROW;
+    pv += kTile * S::ROW;
+    pm += kTile * 8;
+    wr.left -= kTile;
+    if (wr.left <= 0) {
+      wr.next_unit(a);
+      if (wr.left > 0) seek();
     }
   };
-  int issued = 0;
-  for (; issued < min(count, kStages); ++issued) {
-    if (issued > 0) wr.next(a);
-    issue(issued);
+  seek();
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) {
+    if (i < count) issue(i);
+    cp_async_commit();
   }
   Warp<DH, HPL, NB> w;
   w.lr = lane >> 2;
   w.lc = lane & 3;
-  int first = rd.t;  // of the unit in this share
-  w.start(a, rd.b, rd.g);
+  // Columns per head set (HPL = 1): 1, 2 or 4 >= the group's heads.
+  auto columns = [&](int g) {
+    const int H = heads_of_group(a, g);
+    return HPL == 2 || H > 2 ? 4 : H;
+  };
+  int hp = columns(rd.g);
+  w.start(a, rd.b, rd.g, hp);
   int stage = 0;
-  uint32_t phase = 0;
   for (int i = 0; i < count; ++i) {
-    if (!__all_sync(0xffffffffu, mbar_wait(full + stage, phase, abort_flag))) break;
-    const int left = rd.n - rd.t * kTile;
-    const uint8_t* s = ring + stage * S::TILE_BYTES;
-    if (left >= kTile) w.template tile<true>(s, left);
-    else w.template tile<false>(s, left);
+    cp_async_wait<kStages - 1>();
     __syncwarp();
-    if (issued < count) {
-      wr.next(a);
-      issue(stage);
-      ++issued;
-    }
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1u;
-    }
-    const bool end = left <= kTile;
-    if (end || i + 1 == count) {
-      w.finish(a, rd.b, rd.g, first == 0 && end, gw + static_cast<long long>(rd.b) * a.G + rd.g);
-      if (i + 1 == count) break;
-      rd.next(a);
-      first = 0;
-      w.start(a, rd.b, rd.g);
+    const uint8_t* s = sm + warp * S::RING + stage * S::TILE_BYTES;
+    const int left = rd.left;
+    if (HPL == 1 && hp == 1) {
+      if (left >= kTile) w.template tile<1, true>(s, left);
+      else w.template tile<1, false>(s, left);
+    } else if (HPL == 1 && hp == 2) {
+      if (left >= kTile) w.template tile<2, true>(s, left);
+      else w.template tile<2, false>(s, left);
     } else {
-      ++rd.t;
+      if (left >= kTile) w.template tile<4, true>(s, left);
+      else w.template tile<4, false>(s, left);
+    }
+    __syncwarp();
+    if (i + kStages < count) issue(stage);
+    cp_async_commit();
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    rd.left = left - kTile;
+    if (rd.left <= 0 || i + 1 == count) {
+      w.finish(a, rd.b, rd.g, hp, first_whole && rd.left <= 0, gw + static_cast<long long>(rd.b) * a.G + rd.g);
+      if (i + 1 == count) break;
+      rd.next_unit(a);
+      first_whole = true;
+      hp = columns(rd.g);
+      w.start(a, rd.b, rd.g, hp);
     }
   }
 }
