@@ -239,6 +239,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// (x & 0x000f000f) | one in one instruction: with both masks as constants the
+// compiler emits two, so `one` comes from a register that it cannot see into.
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t one) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(x), "r"(one));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -305,6 +312,7 @@ struct Warp {
   float fac[NB][HPL], qsum[NB][HPL];    // of this lane's score columns
   float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4], ones[NB][4];
   int lr, lc;
+  uint32_t k128;  // 0x43004300, bf16 128 twice
 
   __device__ __forceinline__ void start(const AttnArgs& a, int b, int g, int hp) {
     const int H = heads_of_group(a, g);
@@ -495,8 +503,8 @@ struct Warp {
         uint32_t f[4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          f[2 * r] = ((x[2 * hw + r] >> sh) & 0x000f000fu) | 0x43004300u;
-          f[2 * r + 1] = ((x[2 * hw + r] >> (sh + 4)) & 0x000f000fu) | 0x43004300u;
+          f[2 * r] = code_pair(x[2 * hw + r] >> sh, k128);
+          f[2 * r + 1] = code_pair(x[2 * hw + r] >> (sh + 4), k128);
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) mma_bf16(acc[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
@@ -681,6 +689,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   Warp<DH, HPL, NB> w;
   w.lr = lane >> 2;
   w.lc = lane & 3;
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(w.k128));
   // Columns per head set (HPL = 1): 1, 2 or 4 >= the group's heads.
   auto columns = [&](int g) {
     const int H = heads_of_group(a, g);
