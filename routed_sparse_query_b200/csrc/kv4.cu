@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    s = scale_k sum(q n) + zero_k sum(q) in fp32.
 //  - Output, dims x heads, over the keys: 0x4300 | n is the bf16 128 + n. The
 //    weight operand is p scale_v in bf16 (fp16 would not hold the range of the
-//    scales), and sum p scale_v (128 + n) = sum p scale_v (n - 8) + 136 sum of
-//    the same rounded weights (a product with ones); the rest, sum p (zero_v
-//    + 8 scale_v), is kept in fp32. The rounding of p thus meets codes around
+//    scales); 136 times the sum of the same rounded weights is taken off
+//    again, which leaves sum p scale_v (n - 8), and the rest, sum p (zero_v +
+//    8 scale_v), is kept in fp32. The rounding of p thus meets codes around
 //    zero, |n - 8| <= 8.
 //  - Up to 4 heads per group: the heads sit in the even columns, 4 / HP times
 //    over (HP = 1, 2 or 4 >= the group's heads), so the scores' accumulator
@@ -310,7 +310,7 @@ struct Warp {
   static constexpr int SUB = kTile / 16;
   uint32_t qf[NB][KS][2];               // B fragments of the queries (column lr)
   float fac[NB][HPL], qsum[NB][HPL];    // of this lane's score columns
-  float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4], ones[NB][4];
+  float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4];
   int lr, lc;
   uint32_t k128;  // 0x43004300, bf16 128 twice
 
@@ -365,7 +365,6 @@ struct Warp {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ones[nb][i] = 0.0f;
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[nb][t][i] = 0.0f;
       }
@@ -458,7 +457,6 @@ struct Warp {
           const float f = al[nb][j];
           l[nb][j] *= f;
           zs[nb][j] *= f;
-          ones[nb][j] *= f;
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             acc[nb][t][j] *= f;
@@ -483,7 +481,11 @@ struct Warp {
             zs[nb][j] = fmaf(p, vc, zs[nb][j]);
             w2[j] = p * vs;
           }
-          pk[nb][i][r] = pack_bf16x2(w2[0], w2[1]);
+          const uint32_t w = pack_bf16x2(w2[0], w2[1]);
+          pk[nb][i][r] = w;
+#pragma unroll
+          for (int j = 0; j < HPL; ++j)  // the weights as rounded, of the codes' 128 + 8
+            zs[nb][j] = fmaf(-136.0f, __uint_as_float(j == 0 ? w << 16 : w & 0xffff0000u), zs[nb][j]);
         }
       }
 #pragma unroll
@@ -509,9 +511,6 @@ struct Warp {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) mma_bf16(acc[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
       }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        mma_bf16(ones[nb], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, pw[nb][0], pw[nb][1]);
     }
   }
 
@@ -529,7 +528,6 @@ struct Warp {
           if (o < hp) continue;
           ls += __shfl_xor_sync(0xffffffffu, ls, o);
           z += __shfl_xor_sync(0xffffffffu, z, o);
-          ones[nb][j] += __shfl_xor_sync(0xffffffffu, ones[nb][j], o);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             acc[nb][t][j] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j], o);
@@ -542,7 +540,6 @@ struct Warp {
           z += __shfl_xor_sync(0xffffffffu, z, o);
         }
         if (h >= H || (HPL == 1 && h >= hp)) continue;
-        z = fmaf(-136.0f, ones[nb][j], z);
         const float f = whole ? 1.0f / ls : 1.0f;
         float o[DH / 8];  // elements 32 x + 4 lr + {0..3}, x < DH / 32
 #pragma unroll

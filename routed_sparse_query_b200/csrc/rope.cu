@@ -10,10 +10,12 @@
 // Bound by HBM (2 + 2 bytes per element forward, 2 + 4 + 4 backward), so the
 // split serves the loads: d_head / 8 lanes take one token, each with two
 // 4-element chunks chosen so that both members of a rotated pair sit in the
-// same lane (no exchange but the norm's sum), and walk the token's heads, so
+// same lane (no exchange but the norm's sums), and walk the token's heads, so
 // that the angles -- the only expensive arithmetic, see turn() -- are formed
 // once per token and not once per row. Neighbouring lane groups take
-// neighbouring tokens: a warp reads whole 64-byte segments of a head.
+// neighbouring tokens: a warp reads whole 64-byte segments of a head. Several
+// heads' loads are in flight per thread. The norm's weights are multiplied
+// into cos and sin once per token.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -29,43 +31,48 @@ constexpr int kThreads = 256;
 // cos and sin of 2 pi t. The angle of a far position times a frequency needs
 // more than fp32's 24 bits (position 1e6 leaves 0.06 rad of error), so the
 // caller forms t (in turns) in fp64; its fractional part is exact there and
-// then fits fp32 with an error of 2^-25 turns.
+// then fits fp32 with an error of 2^-25 turns. What is left is within half a
+// turn, where the hardware sine and cosine are within 2^-20.
 __device__ __forceinline__ void turn(double t, float scale, float* c, float* s) {
-  float sn, cs;
-  sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &cs);
-  *c = cs * scale;
-  *s = sn * scale;
+  const float x = 6.28318530717958647692f * static_cast<float>(t - rint(t));
+  *c = __cosf(x) * scale;
+  *s = __sinf(x) * scale;
 }
 
+// Lane l of a token: rotated lanes (l < d_rot / 8) hold chunk l and the chunk
+// d_rot / 2 elements further; the others the next two chunks in order. Its 8
+// values are kept as pairs (A_j, B_j), j < 4: element j of the two chunks, or
+// with adjacent pairs elements 2i and 2i + 1 of the chunks one after the other.
 struct Lane {
-  int c0, c1;  // this lane's two chunks of 4 elements
-  bool rot;
+  int c0, c1;
+  bool rot, adjacent;
+  __device__ __forceinline__ int pair(int j) const { return adjacent ? 2 * (j < 2 ? c0 : c1) + (j & 1) : 4 * c0 + j; }
+  __device__ __forceinline__ int elem_a(int j) const { return adjacent ? 4 * (j < 2 ? c0 : c1) + 2 * (j & 1) : 4 * c0 + j; }
+  __device__ __forceinline__ int elem_b(int j) const { return adjacent ? elem_a(j) + 1 : 4 * c1 + j; }
 };
 
-// Lane l of a token: rotated lanes (l < d_rot / 8) hold chunk l and the chunk
-// d_rot / 2 elements further; the others the next two chunks in order.
-__device__ __forceinline__ Lane lane_of(int l, int d_rot) {
-  const int nr = d_rot / 8;
+__device__ __forceinline__ Lane lane_of(int l, const RopeArgs& a) {
+  const int nr = a.d_rot / 8;
   Lane r;
   r.rot = l < nr;
+  r.adjacent = a.adjacent != 0;
   r.c0 = r.rot ? l : 2 * l;
   r.c1 = r.rot ? l + nr : 2 * l + 1;
   return r;
 }
 
-// The four angles of a lane. HALF pairs: element j of c0 with element j of
-// c1, pair 4 c0 + j. Adjacent pairs: (2i, 2i+1) inside each chunk.
-__device__ __forceinline__ void angles(const RopeArgs& a, const Lane& ln, long long row, int b, int t, float (&cs)[4],
-                                       float (&sn)[4]) {
+// The lane's angles; `on`: the token exists (else no rotation: its zeros stay zeros).
+__device__ __forceinline__ void angles(const RopeArgs& a, const Lane& ln, bool on, long long row, int b, int t,
+                                       float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     cs[j] = 1.0f;
     sn[j] = 0.0f;
   }
-  if (!ln.rot) return;
+  if (!ln.rot || !on) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int pair = a.adjacent ? 2 * (j < 2 ? ln.c0 : ln.c1) + (j & 1) : 4 * ln.c0 + j;
+    const int pair = ln.pair(j);
     int ax = a.axis != nullptr ? a.axis[pair] : 0;
     if (ax < 0 || ax >= a.axes) {
       set_status(GQE_ERR_DEVICE_CHECK);
@@ -77,23 +84,46 @@ __device__ __forceinline__ void angles(const RopeArgs& a, const Lane& ln, long l
   }
 }
 
-__device__ __forceinline__ void unpack(uint2 v, float* f) {
-  f[0] = __uint_as_float(v.x << 16);
-  f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16);
-  f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
-// v[0..3] chunk c0, v[4..7] chunk c1; sgn = 1 rotates, -1 rotates back.
-__device__ __forceinline__ void rotate(bool adjacent, const float (&cs)[4], const float (&sn)[4], float sgn,
-                                       float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int ia = adjacent ? 2 * j : j, ib = adjacent ? 2 * j + 1 : j + 4;
-    const float x = v[ia], y = v[ib], s = sgn * sn[j];
-    v[ia] = x * cs[j] - y * s;
-    v[ib] = x * s + y * cs[j];
+// A row's raw words (A0 A1 | A2 A3 | B0 B1 | B2 B3 in chunk order) to pairs
+// and back.
+__device__ __forceinline__ void unpack(const uint2& r0, const uint2& r1, bool adjacent, float (&A)[4], float (&B)[4]) {
+  uint32_t w[4] = {r0.x, r0.y, r1.x, r1.y};
+  if (adjacent) {
+    const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), a1 = __byte_perm(w[2], w[3], 0x5410),
+                   b0 = __byte_perm(w[0], w[1], 0x7632), b1 = __byte_perm(w[2], w[3], 0x7632);
+    w[0] = a0; w[1] = a1; w[2] = b0; w[3] = b1;
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    A[2 * i] = __uint_as_float(w[i] << 16);
+    A[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    B[2 * i] = __uint_as_float(w[2 + i] << 16);
+    B[2 * i + 1] = __uint_as_float(w[2 + i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void pack(const float (&A)[4], const float (&B)[4], bool adjacent, uint2* r0, uint2* r1) {
+  uint32_t w[4] = {pack_bf16x2(A[0], A[1]), pack_bf16x2(A[2], A[3]), pack_bf16x2(B[0], B[1]), pack_bf16x2(B[2], B[3])};
+  if (adjacent) {
+    const uint32_t e0 = __byte_perm(w[0], w[2], 0x5410), e1 = __byte_perm(w[0], w[2], 0x7632),
+                   e2 = __byte_perm(w[1], w[3], 0x5410), e3 = __byte_perm(w[1], w[3], 0x7632);
+    w[0] = e0; w[1] = e1; w[2] = e2; w[3] = e3;
+  }
+  *r0 = make_uint2(w[0], w[1]);
+  *r1 = make_uint2(w[2], w[3]);
+}
+// The same for fp32 chunks x, y.
+__device__ __forceinline__ void to_pairs(const float4& x, const float4& y, bool adjacent, float (&A)[4], float (&B)[4]) {
+  A[0] = x.x; B[3] = y.w;
+  A[1] = adjacent ? x.z : x.y;
+  A[2] = adjacent ? y.x : x.z;
+  A[3] = adjacent ? y.z : x.w;
+  B[0] = adjacent ? x.y : y.x;
+  B[1] = adjacent ? x.w : y.y;
+  B[2] = adjacent ? y.y : y.z;
+}
+__device__ __forceinline__ void from_pairs(const float (&A)[4], const float (&B)[4], bool adjacent, float4* x, float4* y) {
+  *x = adjacent ? make_float4(A[0], B[0], A[1], B[1]) : make_float4(A[0], A[1], A[2], A[3]);
+  *y = adjacent ? make_float4(A[2], B[2], A[3], B[3]) : make_float4(B[0], B[1], B[2], B[3]);
 }
 
 template <int LPT>
@@ -103,27 +133,11 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// The operand (0: routed queries, 1: shared head, 2: keys) and the head
-// inside it of the flat head index h.
-__device__ __forceinline__ int operand_of(const RopeArgs& a, int h, int* hh) {
-  if (h < a.n[0]) {
-    *hh = h;
-    return 0;
-  }
-  if (h < a.n[0] + a.n[1]) {
-    *hh = 0;
-    return 1;
-  }
-  *hh = h - a.n[0] - a.n[1];
-  return 2;
-}
-
-__device__ __forceinline__ long long offset_of(const RopeRows& r, int b, int t, int h) {
-  return b * r.sb + h * r.sh + t * r.st;
-}
-// Token-list order (slot_pos from the dispatch): the row's list entry, or -1
-// (recorded) where it does not name one.
-__device__ __forceinline__ long long list_offset(const RopeArgs& a, long long row, int h, int dh) {
+// Offset of a row of operand op (head h), or -1: in token-list order
+// (slot_pos from the dispatch) a list entry that does not exist (recorded).
+__device__ __forceinline__ long long row_offset(const RopeArgs& a, const RopeRows& r, int op, long long row, int b, int t,
+                                                int h, int dh) {
+  if (op != 0 || a.slot_pos == nullptr) return b * r.sb + h * r.sh + t * r.st;
   const int32_t e = a.slot_pos[row * a.n[0] + h];
   if (e < 0 || e >= a.R * a.n[0]) {
     set_status(GQE_ERR_DEVICE_CHECK);
@@ -132,64 +146,107 @@ __device__ __forceinline__ long long list_offset(const RopeArgs& a, long long ro
   return static_cast<long long>(e) * dh;
 }
 
-template <int DH>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
-  constexpr int LPT = DH / 8, TOK = kThreads / LPT;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int l = threadIdx.x % LPT;
-  const long long row = static_cast<long long>(blockIdx.x) * TOK + threadIdx.x / LPT;
-  const bool on = row < a.R;
-  const int b = on ? static_cast<int>(row / a.T) : 0, t = on ? static_cast<int>(row - static_cast<long long>(b) * a.T) : 0;
-  const Lane ln = lane_of(l, a.d_rot);
-  float cs[4], sn[4];
-  if (on) angles(a, ln, row, b, t, cs, sn);
-  const int H = a.n[0] + a.n[1] + a.n[2];
-  const int h1 = min(H, (static_cast<int>(blockIdx.y) + 1) * a.hpc);
-  for (int h = blockIdx.y * a.hpc; h < h1; ++h) {
-    int hh;
-    const int op = operand_of(a, h, &hh);
-    const float* w = op == 2 ? a.w_k : a.w_q;
-    float v[8];
-    uint2 r0 = make_uint2(0u, 0u), r1 = r0;
-    const bool list = op == 0 && a.slot_pos != nullptr;
-    const long long lo = list && on ? list_offset(a, row, hh, DH) : 0;
-    const bool live = on && lo >= 0;
-    if (live) {
-      const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + (list ? lo : offset_of(a.x[op], b, t, hh));
-      r0 = *reinterpret_cast<const uint2*>(p + 4 * ln.c0);
-      r1 = *reinterpret_cast<const uint2*>(p + 4 * ln.c1);
-    }
-    unpack(r0, v);
-    unpack(r1, v + 4);
-    if (a.norm) {
-      float s = 0.0f;
+// One operand's heads [h0, h1) of this lane group's token, U rows in flight.
+template <int DH, int U>
+__device__ __forceinline__ void rope_rows_fwd(const RopeArgs& a, const Lane& ln, int op, int h0, int h1, bool on,
+                                              long long row, int b, int t, const float (&ca)[4], const float (&sb)[4],
+                                              const float (&sa)[4], const float (&cb)[4]) {
+  constexpr int LPT = DH / 8;
+  for (int h = h0; h < h1; h += U) {
+    uint2 r0[U], r1[U];
+    long long off[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
-      const float rstd = rsqrtf(lane_sum<LPT>(s) * (1.0f / DH) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float wi = w != nullptr ? __ldg(w + 4 * (i < 4 ? ln.c0 : ln.c1) + (i & 3)) : 1.0f;
-        v[i] = v[i] * rstd * wi;
+    for (int u = 0; u < U; ++u) {
+      off[u] = on ? row_offset(a, a.x[op], op, row, b, t, h + u, DH) : -1;
+      r0[u] = r1[u] = make_uint2(0u, 0u);
+      if (off[u] >= 0) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + off[u];
+        r0[u] = *reinterpret_cast<const uint2*>(p + 4 * ln.c0);
+        r1[u] = *reinterpret_cast<const uint2*>(p + 4 * ln.c1);
       }
     }
-    if (!live) continue;
-    if (ln.rot) rotate(a.adjacent, cs, sn, 1.0f, v);
-    uint16_t* q = static_cast<uint16_t*>(a.y[op].p) + (list ? lo : offset_of(a.y[op], b, t, hh));
-    *reinterpret_cast<uint2*>(q + 4 * ln.c0) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    *reinterpret_cast<uint2*>(q + 4 * ln.c1) = make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float A[4], B[4];
+      unpack(r0[u], r1[u], ln.adjacent, A, B);
+      if (a.norm) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(A[j], A[j], fmaf(B[j], B[j], s));
+        const float rstd = rsqrtf(fmaf(lane_sum<LPT>(s), 1.0f / DH, a.eps));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          A[j] *= rstd;
+          B[j] *= rstd;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = A[j], y = B[j];
+        // Elements that are not rotated do not meet their neighbour (0 * inf).
+        A[j] = ln.rot ? fmaf(x, ca[j], -y * sb[j]) : x * ca[j];
+        B[j] = ln.rot ? fmaf(x, sa[j], y * cb[j]) : y * cb[j];
+      }
+      if (off[u] < 0) continue;
+      pack(A, B, ln.adjacent, &r0[u], &r1[u]);
+      // In token-list order inputs and outputs share their offsets.
+      const long long o = op == 0 && a.slot_pos != nullptr ? off[u] : row_offset(a, a.y[op], 1, row, b, t, h + u, DH);
+      uint16_t* q = static_cast<uint16_t*>(a.y[op].p) + o;
+      *reinterpret_cast<uint2*>(q + 4 * ln.c0) = r0[u];
+      *reinterpret_cast<uint2*>(q + 4 * ln.c1) = r1[u];
+    }
   }
 }
 
-// Sum of a gradient row's parts (see RopeGrad), this lane's 8 elements.
-__device__ __forceinline__ void load_grad(const RopeGrad& g, long long off, int hh, const Lane& ln, float (&v)[8]) {
+template <int DH>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+  constexpr int LPT = DH / 8, TOK = kThreads / LPT, U = 4;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row = static_cast<long long>(blockIdx.x) * TOK + threadIdx.x / LPT;
+  const bool on = row < a.R;
+  const int b = on ? static_cast<int>(row / a.T) : 0, t = on ? static_cast<int>(row - static_cast<long long>(b) * a.T) : 0;
+  const Lane ln = lane_of(threadIdx.x % LPT, a);
+  float cs[4], sn[4];
+  angles(a, ln, on, row, b, t, cs, sn);
+  const int first = blockIdx.y * a.hpc, last = first + a.hpc;  // this CTA's heads of all operands
+  int at = 0;
+#pragma unroll 1
+  for (int op = 0; op < 3; ++op) {
+    const int h0 = max(first - at, 0), h1 = min(last - at, a.n[op]);
+    at += a.n[op];
+    if (h0 >= h1) continue;
+    const float* w = a.norm ? (op == 2 ? a.w_k : a.w_q) : nullptr;
+    float ca[4], sb[4], sa[4], cb[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  const float* base = static_cast<const float*>(g.rows.p) + off;
+    for (int j = 0; j < 4; ++j) {
+      const float wa = w != nullptr ? __ldg(w + ln.elem_a(j)) : 1.0f, wb = w != nullptr ? __ldg(w + ln.elem_b(j)) : 1.0f;
+      ca[j] = cs[j] * wa;
+      sb[j] = sn[j] * wb;
+      sa[j] = sn[j] * wa;
+      cb[j] = cs[j] * wb;
+    }
+    const int mid = h0 + (h1 - h0) / U * U;
+    rope_rows_fwd<DH, U>(a, ln, op, h0, mid, on, row, b, t, ca, sb, sa, cb);
+    rope_rows_fwd<DH, 1>(a, ln, op, mid, h1, on, row, b, t, ca, sb, sa, cb);
+  }
+}
+
+// The next row's operands of the backward, loaded while one is worked on.
+struct BwdRow {
+  float4 g0, g1;
+  uint2 x0, x1;
+  long long off;
+};
+
+// Sum of a gradient row's parts (see RopeGrad), this lane's 8 elements.
+__device__ __forceinline__ void load_parts(const RopeGrad& g, const float* base, int hh, const Lane& ln, float4* x,
+                                           float4* y) {
+  *x = *y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add = [&](const float* p) {
-    const float4 x = *reinterpret_cast<const float4*>(p + 4 * ln.c0), y = *reinterpret_cast<const float4*>(p + 4 * ln.c1);
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    const float4 u = *reinterpret_cast<const float4*>(p + 4 * ln.c0), v = *reinterpret_cast<const float4*>(p + 4 * ln.c1);
+    x->x += u.x; x->y += u.y; x->z += u.z; x->w += u.w;
+    y->x += v.x; y->y += v.y; y->z += v.z; y->w += v.w;
   };
   for (int f = 0; f < g.parts; ++f) {
     for (int s = 0; s < g.streams; ++s) add(base + f * g.part_stride + s * g.stream_stride);
@@ -197,88 +254,126 @@ __device__ __forceinline__ void load_grad(const RopeGrad& g, long long off, int 
   }
 }
 
-template <int DH>
+// PARTS: the gradients come in parts (the layer's backward).
+template <int DH, bool PARTS>
 __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(RopeArgs a, RopeBwdArgs d) {
   constexpr int LPT = DH / 8, TOK = kThreads / LPT;
   __shared__ float red[kThreads / 32][2][DH];
-  const int l = threadIdx.x % LPT;
-  const Lane ln = lane_of(l, a.d_rot);
+  const Lane ln = lane_of(threadIdx.x % LPT, a);
   const int H = a.n[0] + a.n[1] + a.n[2];
   const long long tiles = (a.R + TOK - 1) / TOK;
   const int chunks = (H + a.hpc - 1) / a.hpc;
-  float dwq[8], dwk[8];
+  float dwa[2][4], dwb[2][4];  // queries', keys' weight gradients
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.0f;
+  for (int i = 0; i < 8; ++i) dwa[i / 4][i % 4] = dwb[i / 4][i % 4] = 0.0f;
   for (long long it = blockIdx.x; it < tiles * chunks; it += gridDim.x) {
     const long long tile = it / chunks;
-    const int ch = static_cast<int>(it - tile * chunks);
+    const int first = static_cast<int>(it - tile * chunks) * a.hpc, last = first + a.hpc;
     const long long row = tile * TOK + threadIdx.x / LPT;
     const bool on = row < a.R;
     const int b = on ? static_cast<int>(row / a.T) : 0,
               t = on ? static_cast<int>(row - static_cast<long long>(b) * a.T) : 0;
     float cs[4], sn[4];
-    if (on) angles(a, ln, row, b, t, cs, sn);
-    const int h1 = min(H, (ch + 1) * a.hpc);
-    for (int h = ch * a.hpc; h < h1; ++h) {
-      int hh;
-      const int op = operand_of(a, h, &hh);
-      const bool list = op == 0 && a.slot_pos != nullptr;
-      const long long lo = list && on ? list_offset(a, row, hh, DH) : 0;
-      const bool live = on && lo >= 0;
-      const float* w = op == 2 ? a.w_k : a.w_q;
-      float g[8], x[8];
+    angles(a, ln, on, row, b, t, cs, sn);
+    int at = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = x[i] = 0.0f;
-      if (live) {
-        load_grad(d.g[op], list ? lo : offset_of(d.g[op].rows, b, t, hh), hh, ln, g);
-        if (ln.rot) rotate(a.adjacent, cs, sn, -1.0f, g);
+    for (int op = 0; op < 3; ++op) {
+      constexpr int kQueries = 0, kKeys = 1;
+      const int wi = op == 2 ? kKeys : kQueries;
+      const int h0 = max(first - at, 0), h1 = min(last - at, a.n[op]);
+      at += a.n[op];
+      if (h0 >= h1) continue;
+      const float* w = a.norm ? (op == 2 ? a.w_k : a.w_q) : nullptr;
+      float wa[4], wb[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        wa[j] = w != nullptr ? __ldg(w + ln.elem_a(j)) : 1.0f;
+        wb[j] = w != nullptr ? __ldg(w + ln.elem_b(j)) : 1.0f;
+      }
+      auto load = [&](int h, BwdRow* r) {
+        r->off = on ? row_offset(a, a.x[op], op, row, b, t, h, DH) : -1;
+        r->g0 = r->g1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        r->x0 = r->x1 = make_uint2(0u, 0u);
+        if (r->off < 0) return;
+        const bool list = op == 0 && a.slot_pos != nullptr;
+        const float* g = static_cast<const float*>(d.g[op].rows.p) + (list ? r->off : row_offset(a, d.g[op].rows, 1, row, b, t, h, DH));
+        if constexpr (PARTS) {
+          load_parts(d.g[op], g, h, ln, &r->g0, &r->g1);
+        } else {
+          r->g0 = *reinterpret_cast<const float4*>(g + 4 * ln.c0);
+          r->g1 = *reinterpret_cast<const float4*>(g + 4 * ln.c1);
+        }
         if (a.norm) {
-          const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + (list ? lo : offset_of(a.x[op], b, t, hh));
-          unpack(*reinterpret_cast<const uint2*>(p + 4 * ln.c0), x);
-          unpack(*reinterpret_cast<const uint2*>(p + 4 * ln.c1), x + 4);
+          const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + r->off;
+          r->x0 = *reinterpret_cast<const uint2*>(p + 4 * ln.c0);
+          r->x1 = *reinterpret_cast<const uint2*>(p + 4 * ln.c1);
         }
-      }
-      if (a.norm) {
-        float s = 0.0f, gx = 0.0f;
+      };
+      BwdRow next;
+      load(h0, &next);
+      for (int h = h0; h < h1; ++h) {
+        const BwdRow r = next;
+        if (h + 1 < h1) load(h + 1, &next);
+        float A[4], B[4];
+        to_pairs(r.g0, r.g1, ln.adjacent, A, B);
+        if (ln.rot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-        const float rstd = rsqrtf(lane_sum<LPT>(s) * (1.0f / DH) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= rstd;
-          const float dw = live ? g[i] * x[i] : 0.0f;
-          if (op == 2) dwk[i] += dw;
-          else dwq[i] += dw;
-          if (w != nullptr) g[i] *= __ldg(w + 4 * (i < 4 ? ln.c0 : ln.c1) + (i & 3));
-          gx = fmaf(g[i], x[i], gx);
+          for (int j = 0; j < 4; ++j) {
+            const float x = A[j], y = B[j];
+            A[j] = fmaf(x, cs[j], y * sn[j]);
+            B[j] = fmaf(y, cs[j], -x * sn[j]);
+          }
         }
-        gx = lane_sum<LPT>(gx) * (1.0f / DH);
+        if (a.norm) {
+          float X[4], Y[4], s = 0.0f, gx = 0.0f;
+          unpack(r.x0, r.x1, ln.adjacent, X, Y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = rstd * (g[i] - x[i] * gx);
+          for (int j = 0; j < 4; ++j) {
+            s = fmaf(X[j], X[j], fmaf(Y[j], Y[j], s));
+            gx = fmaf(A[j] * wa[j], X[j], fmaf(B[j] * wb[j], Y[j], gx));
+          }
+          s = lane_sum<LPT>(s);
+          gx = lane_sum<LPT>(gx);
+          // An absent row (zeros) adds nothing to the sums, eps = 0 included.
+          const float rstd = r.off < 0 ? 0.0f : rsqrtf(fmaf(s, 1.0f / DH, a.eps));
+          const float mean = gx * rstd * (1.0f / DH);  // of gw xh
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            X[j] *= rstd;
+            Y[j] *= rstd;
+            dwa[wi][j] = fmaf(A[j], X[j], dwa[wi][j]);  // 0 where the row is absent
+            dwb[wi][j] = fmaf(B[j], Y[j], dwb[wi][j]);
+            A[j] = rstd * fmaf(-X[j], mean, A[j] * wa[j]);
+            B[j] = rstd * fmaf(-Y[j], mean, B[j] * wb[j]);
+          }
+        }
+        if (r.off < 0) continue;
+        const bool list = op == 0 && a.slot_pos != nullptr;
+        float* q = static_cast<float*>(a.y[op].p) + (list ? r.off : row_offset(a, a.y[op], 1, row, b, t, h, DH));
+        float4 o0, o1;
+        from_pairs(A, B, ln.adjacent, &o0, &o1);
+        *reinterpret_cast<float4*>(q + 4 * ln.c0) = o0;
+        *reinterpret_cast<float4*>(q + 4 * ln.c1) = o1;
       }
-      if (!live) continue;
-      float* q = static_cast<float*>(a.y[op].p) + (list ? lo : offset_of(a.y[op], b, t, hh));
-      *reinterpret_cast<float4*>(q + 4 * ln.c0) = make_float4(g[0], g[1], g[2], g[3]);
-      *reinterpret_cast<float4*>(q + 4 * ln.c1) = make_float4(g[4], g[5], g[6], g[7]);
     }
   }
   if (d.part == nullptr) return;
   // The weights' gradients: lanes of one column over the warp's tokens, then
   // the warps, in a fixed order; one partial row per CTA.
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int o = LPT; o < 32; o <<= 1) {
-      dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-      dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
-    }
   const int warp = threadIdx.x / 32;
-  if (threadIdx.x % 32 < LPT)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = 4 * (i < 4 ? ln.c0 : ln.c1) + (i & 3);
-      red[warp][0][col] = dwq[i];
-      red[warp][1][col] = dwk[i];
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int o = LPT; o < 32; o <<= 1) {
+        dwa[i][j] += __shfl_xor_sync(0xffffffffu, dwa[i][j], o);
+        dwb[i][j] += __shfl_xor_sync(0xffffffffu, dwb[i][j], o);
+      }
+      if (threadIdx.x % 32 < LPT) {
+        red[warp][i][ln.elem_a(j)] = dwa[i][j];
+        red[warp][i][ln.elem_b(j)] = dwb[i][j];
+      }
     }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * DH; i += kThreads) {
@@ -345,8 +440,11 @@ int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* 
   const bool dw = a.norm && (dw_q != nullptr || dw_k != nullptr);
   d.part = dw ? static_cast<float*>(ws) : nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dh == 64) rope_bwd_kernel<64><<<ctas, rope_impl::kThreads, 0, st>>>(a, d);
-  else rope_bwd_kernel<32><<<ctas, rope_impl::kThreads, 0, st>>>(a, d);
+  bool parts = false;
+  for (int i = 0; i < 3; ++i) parts = parts || d.g[i].parts * d.g[i].streams != 1 || d.g[i].extra != 0;
+  auto kernel = dh == 64 ? (parts ? rope_bwd_kernel<64, true> : rope_bwd_kernel<64, false>)
+                         : (parts ? rope_bwd_kernel<32, true> : rope_bwd_kernel<32, false>);
+  kernel<<<ctas, rope_impl::kThreads, 0, st>>>(a, d);
   if (dw && dh == 64) rope_dw_kernel<64><<<2 * 64 / 4, rope_impl::kThreads, 0, st>>>(d.part, ctas, dw_q, dw_k);
   if (dw && dh == 32) rope_dw_kernel<32><<<2 * 32 / 4, rope_impl::kThreads, 0, st>>>(d.part, ctas, dw_q, dw_k);
   return cudaGetLastError();

@@ -229,6 +229,37 @@ def test_rows_of_zeros_and_of_large_values(rsq):
     assert abs(float((y[2] ** 2).mean()) - 1) < 2 ** -6
 
 
+def test_eps_of_zero_and_a_partial_tile(rsq):
+    # Tokens behind the last one add nothing to the weights' gradients, although
+    # a row of zeros has no norm with eps = 0.
+    cfg = rsq.GQEConfig(1, 5, 64, 2, 1, 1, 64, 0)
+    gen = torch.Generator().manual_seed(6)
+    K, g = torch.randn(1, 2, 5, 64, generator=gen).to(torch.bfloat16), torch.randn(1, 2, 5, 64, generator=gen)
+    rope = rsq.GQERope.of(0, torch.empty(0, dtype=torch.float64, device="cuda"), eps=0.0, flags=rsq.GQE_ROPE_NORM)
+    ws = torch.empty(rsq.gqe_workspace_bytes(cfg, rsq.GQE_WS_QK_ROPE), dtype=torch.uint8, device="cuda")
+    dk, dw = torch.empty(1, 2, 5, 64, device="cuda"), torch.empty(64, device="cuda")
+    rsq.gqe_qk_rope_bwd(cfg, rope, None, None, K.cuda(), None, None, None, g.cuda(), None, None, dk, None, dw, ws)
+    dx, dwr = op.rope_backward(f64(K), f64(g), np.zeros((5, 0)), norm=True)
+    assert np.abs(dk.cpu().double().numpy() - dx).max() <= 2.0 ** -16 * np.abs(dx).max()
+    size = np.abs(f64(g) * op.rope_norm(f64(K), 1.0, 0.0)).reshape(-1, 64).sum(0)
+    assert (np.abs(dw.cpu().double().numpy() - dwr) <= 2.0 ** -16 * size).all()
+
+
+def test_passed_elements_do_not_meet_their_neighbours(rsq):
+    # Without the norm an infinity stays in its element (or its rotated pair).
+    cfg = rsq.GQEConfig(1, 3, 64, 1, 1, 1, 64, 0)
+    K = torch.randn(1, 1, 3, 64, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    K[..., 40] = float("inf")
+    K[..., 63] = float("nan")
+    for flags in (0, rsq.GQE_ROPE_ADJACENT):
+        rope = rsq.GQERope.of(16, torch.ones(8, dtype=torch.float64, device="cuda"), flags=flags)
+        y = torch.empty_like(K, device="cuda")
+        rsq.gqe_qk_rope(cfg, rope, None, None, K.cuda(), None, None, None, y)
+        y = y.cpu()
+        keep = [i for i in range(16, 64) if i != 63]
+        assert torch.equal(y[..., keep], K[..., keep]) and torch.isfinite(y[..., :16].float()).all()
+
+
 def test_streams_and_graph_capture(rsq):
     case = CASES["odd_dh32"]
     B, T, G, k, dh = case[:5]
