@@ -231,9 +231,12 @@ struct RopeGrad {
 };
 struct RopeBwdArgs {
   RopeGrad g[3];
-  float* part;  // [CTAs][2][d_head] partial weight gradients (set by the launcher)
+  float* part;  // [CTAs][d_head] partial weight gradients (set by the launcher)
+  int cq, hpc_k;  // CTAs of the queries, heads per item of the keys (set by the launcher)
 };
 constexpr int kRopeCtas = 148 * 8;  // CTAs of 256 threads that fill the SMs
+constexpr int kRopeBwdPerSm = 4;
+constexpr int kRopeBwdCtas = 148 * kRopeBwdPerSm;
 int rope_fwd(RopeArgs a, int dh, void* stream);
 size_t rope_bwd_ws_bytes(int dh);
 int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* ws, void* stream);

@@ -13,8 +13,10 @@
 // same lane (no exchange but the norm's sums), and walk the token's heads, so
 // that the angles -- the only expensive arithmetic, see turn() -- are formed
 // once per token and not once per row. Neighbouring lane groups take
-// neighbouring tokens: a warp reads whole 64-byte segments of a head. Several
-// heads' loads are in flight per thread. The norm's weights are multiplied
+// neighbouring tokens: a warp reads whole 64-byte segments of a head. Bytes in
+// flight come from four rows per thread in the forward, from many threads in
+// the backward (64 registers; two or more rows per thread cost occupancy and
+// were no faster, nor were rows ahead through shared memory). The norm's weights are multiplied
 // into cos and sin once per token.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -43,6 +45,11 @@ __device__ __forceinline__ void turn(double t, float scale, float* c, float* s) 
 // d_rot / 2 elements further; the others the next two chunks in order. Its 8
 // values are kept as pairs (A_j, B_j), j < 4: element j of the two chunks, or
 // with adjacent pairs elements 2i and 2i + 1 of the chunks one after the other.
+//
+// USUAL: the norm, pairs half the head apart and every element rotated -- what
+// most models do -- are known at compile time; else they are looked at for
+// every row (256k tokens: 181 us against 230).
+template <bool USUAL>
 struct Lane {
   int c0, c1;
   bool rot, adjacent;
@@ -51,18 +58,20 @@ struct Lane {
   __device__ __forceinline__ int elem_b(int j) const { return adjacent ? elem_a(j) + 1 : 4 * c1 + j; }
 };
 
-__device__ __forceinline__ Lane lane_of(int l, const RopeArgs& a) {
-  const int nr = a.d_rot / 8;
-  Lane r;
-  r.rot = l < nr;
-  r.adjacent = a.adjacent != 0;
+template <int DH, bool USUAL>
+__device__ __forceinline__ Lane<USUAL> lane_of(int l, const RopeArgs& a) {
+  const int nr = USUAL ? DH / 8 : a.d_rot / 8;
+  Lane<USUAL> r;
+  r.rot = USUAL || l < nr;
+  r.adjacent = !USUAL && a.adjacent != 0;
   r.c0 = r.rot ? l : 2 * l;
   r.c1 = r.rot ? l + nr : 2 * l + 1;
   return r;
 }
 
 // The lane's angles; `on`: the token exists (else no rotation: its zeros stay zeros).
-__device__ __forceinline__ void angles(const RopeArgs& a, const Lane& ln, bool on, long long row, int b, int t,
+template <bool USUAL>
+__device__ __forceinline__ void angles(const RopeArgs& a, const Lane<USUAL>& ln, bool on, long long row, int b, int t,
                                        float (&cs)[4], float (&sn)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -133,11 +142,9 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Offset of a row of operand op (head h), or -1: in token-list order
-// (slot_pos from the dispatch) a list entry that does not exist (recorded).
-__device__ __forceinline__ long long row_offset(const RopeArgs& a, const RopeRows& r, int op, long long row, int b, int t,
-                                                int h, int dh) {
-  if (op != 0 || a.slot_pos == nullptr) return b * r.sb + h * r.sh + t * r.st;
+// Token-list order (slot_pos from the dispatch): offset of the row of head h,
+// or -1 for a list entry that does not exist (recorded).
+__device__ __forceinline__ long long list_offset(const RopeArgs& a, long long row, int h, int dh) {
   const int32_t e = a.slot_pos[row * a.n[0] + h];
   if (e < 0 || e >= a.R * a.n[0]) {
     set_status(GQE_ERR_DEVICE_CHECK);
@@ -146,67 +153,70 @@ __device__ __forceinline__ long long row_offset(const RopeArgs& a, const RopeRow
   return static_cast<long long>(e) * dh;
 }
 
-// One operand's heads [h0, h1) of this lane group's token, U rows in flight.
-template <int DH, int U>
-__device__ __forceinline__ void rope_rows_fwd(const RopeArgs& a, const Lane& ln, int op, int h0, int h1, bool on,
-                                              long long row, int b, int t, const float (&ca)[4], const float (&sb)[4],
-                                              const float (&sa)[4], const float (&cb)[4]) {
+// Coefficients of a lane's pairs for one operand: (x, y) -> (ca x - sb y, sa x + cb y).
+struct Coef {
+  float ca[4], sb[4], sa[4], cb[4];
+};
+
+// U rows of one lane group's token: inputs at p + u ps, outputs at q + u qs.
+template <int DH, bool USUAL, int U>
+__device__ __forceinline__ void rope_group(const RopeArgs& a, const Lane<USUAL>& ln, const Coef& c, bool live,
+                                           const uint16_t* p, long long ps, uint16_t* q, long long qs) {
   constexpr int LPT = DH / 8;
-  for (int h = h0; h < h1; h += U) {
-    uint2 r0[U], r1[U];
-    long long off[U];
+  uint2 r0[U], r1[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      off[u] = on ? row_offset(a, a.x[op], op, row, b, t, h + u, DH) : -1;
-      r0[u] = r1[u] = make_uint2(0u, 0u);
-      if (off[u] >= 0) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + off[u];
-        r0[u] = *reinterpret_cast<const uint2*>(p + 4 * ln.c0);
-        r1[u] = *reinterpret_cast<const uint2*>(p + 4 * ln.c1);
+  for (int u = 0; u < U; ++u) {
+    r0[u] = r1[u] = make_uint2(0u, 0u);
+    if (live) {
+      r0[u] = *reinterpret_cast<const uint2*>(p + u * ps + 4 * ln.c0);
+      r1[u] = *reinterpret_cast<const uint2*>(p + u * ps + 4 * ln.c1);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float A[4], B[4];
+    unpack(r0[u], r1[u], ln.adjacent, A, B);
+    if (USUAL || a.norm) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s = fmaf(A[j], A[j], fmaf(B[j], B[j], s));
+      const float rstd = rsqrtf(fmaf(lane_sum<LPT>(s), 1.0f / DH, a.eps));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        A[j] *= rstd;
+        B[j] *= rstd;
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float A[4], B[4];
-      unpack(r0[u], r1[u], ln.adjacent, A, B);
-      if (a.norm) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s = fmaf(A[j], A[j], fmaf(B[j], B[j], s));
-        const float rstd = rsqrtf(fmaf(lane_sum<LPT>(s), 1.0f / DH, a.eps));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          A[j] *= rstd;
-          B[j] *= rstd;
-        }
-      }
+    if (ln.rot) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float x = A[j], y = B[j];
-        // Elements that are not rotated do not meet their neighbour (0 * inf).
-        A[j] = ln.rot ? fmaf(x, ca[j], -y * sb[j]) : x * ca[j];
-        B[j] = ln.rot ? fmaf(x, sa[j], y * cb[j]) : y * cb[j];
+        A[j] = fmaf(x, c.ca[j], -y * c.sb[j]);
+        B[j] = fmaf(x, c.sa[j], y * c.cb[j]);
       }
-      if (off[u] < 0) continue;
-      pack(A, B, ln.adjacent, &r0[u], &r1[u]);
-      // In token-list order inputs and outputs share their offsets.
-      const long long o = op == 0 && a.slot_pos != nullptr ? off[u] : row_offset(a, a.y[op], 1, row, b, t, h + u, DH);
-      uint16_t* q = static_cast<uint16_t*>(a.y[op].p) + o;
-      *reinterpret_cast<uint2*>(q + 4 * ln.c0) = r0[u];
-      *reinterpret_cast<uint2*>(q + 4 * ln.c1) = r1[u];
+    } else {  // elements that are not rotated do not meet their neighbour (0 * inf)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        A[j] *= c.ca[j];
+        B[j] *= c.cb[j];
+      }
     }
+    if (!live) continue;
+    pack(A, B, ln.adjacent, &r0[u], &r1[u]);
+    *reinterpret_cast<uint2*>(q + u * qs + 4 * ln.c0) = r0[u];
+    *reinterpret_cast<uint2*>(q + u * qs + 4 * ln.c1) = r1[u];
   }
 }
 
-template <int DH>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
+template <int DH, bool USUAL>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a) {
   constexpr int LPT = DH / 8, TOK = kThreads / LPT, U = 4;
   pdl_wait();
   pdl_launch_dependents();
   const long long row = static_cast<long long>(blockIdx.x) * TOK + threadIdx.x / LPT;
   const bool on = row < a.R;
   const int b = on ? static_cast<int>(row / a.T) : 0, t = on ? static_cast<int>(row - static_cast<long long>(b) * a.T) : 0;
-  const Lane ln = lane_of(threadIdx.x % LPT, a);
+  const Lane<USUAL> ln = lane_of<DH, USUAL>(threadIdx.x % LPT, a);
   float cs[4], sn[4];
   angles(a, ln, on, row, b, t, cs, sn);
   const int first = blockIdx.y * a.hpc, last = first + a.hpc;  // this CTA's heads of all operands
@@ -216,31 +226,39 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a) {
     const int h0 = max(first - at, 0), h1 = min(last - at, a.n[op]);
     at += a.n[op];
     if (h0 >= h1) continue;
-    const float* w = a.norm ? (op == 2 ? a.w_k : a.w_q) : nullptr;
-    float ca[4], sb[4], sa[4], cb[4];
+    const float* w = USUAL || a.norm ? (op == 2 ? a.w_k : a.w_q) : nullptr;
+    Coef c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float wa = w != nullptr ? __ldg(w + ln.elem_a(j)) : 1.0f, wb = w != nullptr ? __ldg(w + ln.elem_b(j)) : 1.0f;
-      ca[j] = cs[j] * wa;
-      sb[j] = sn[j] * wb;
-      sa[j] = sn[j] * wa;
-      cb[j] = cs[j] * wb;
+      c.ca[j] = cs[j] * wa;
+      c.sb[j] = sn[j] * wb;
+      c.sa[j] = sn[j] * wa;
+      c.cb[j] = cs[j] * wb;
     }
-    const int mid = h0 + (h1 - h0) / U * U;
-    rope_rows_fwd<DH, U>(a, ln, op, h0, mid, on, row, b, t, ca, sb, sa, cb);
-    rope_rows_fwd<DH, 1>(a, ln, op, mid, h1, on, row, b, t, ca, sb, sa, cb);
+    const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p);
+    uint16_t* q = static_cast<uint16_t*>(a.y[op].p);
+    if (!USUAL && op == 0 && a.slot_pos != nullptr) {  // token-list order: inputs and outputs at the same rows
+      for (int h = h0; h < h1; ++h) {
+        const long long o = on ? list_offset(a, row, h, DH) : -1;
+        rope_group<DH, USUAL, 1>(a, ln, c, o >= 0, p + o, 0, q + o, 0);
+      }
+      continue;
+    }
+    const long long ps = a.x[op].sh, qs = a.y[op].sh;
+    p += b * a.x[op].sb + t * a.x[op].st + h0 * ps;
+    q += b * a.y[op].sb + t * a.y[op].st + h0 * qs;
+    int h = h0;
+#pragma unroll 1
+    for (; h + U <= h1; h += U, p += U * ps, q += U * qs) rope_group<DH, USUAL, U>(a, ln, c, on, p, ps, q, qs);
+#pragma unroll 1
+    for (; h < h1; ++h, p += ps, q += qs) rope_group<DH, USUAL, 1>(a, ln, c, on, p, 0, q, 0);
   }
 }
 
-// The next row's operands of the backward, loaded while one is worked on.
-struct BwdRow {
-  float4 g0, g1;
-  uint2 x0, x1;
-  long long off;
-};
-
 // Sum of a gradient row's parts (see RopeGrad), this lane's 8 elements.
-__device__ __forceinline__ void load_parts(const RopeGrad& g, const float* base, int hh, const Lane& ln, float4* x,
+template <bool USUAL>
+__device__ __forceinline__ void load_parts(const RopeGrad& g, const float* base, int hh, const Lane<USUAL>& ln, float4* x,
                                            float4* y) {
   *x = *y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add = [&](const float* p) {
@@ -254,143 +272,163 @@ __device__ __forceinline__ void load_parts(const RopeGrad& g, const float* base,
   }
 }
 
-// PARTS: the gradients come in parts (the layer's backward).
-template <int DH, bool PARTS>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(RopeArgs a, RopeBwdArgs d) {
-  constexpr int LPT = DH / 8, TOK = kThreads / LPT;
-  __shared__ float red[kThreads / 32][2][DH];
-  const Lane ln = lane_of(threadIdx.x % LPT, a);
-  const int H = a.n[0] + a.n[1] + a.n[2];
-  const long long tiles = (a.R + TOK - 1) / TOK;
-  const int chunks = (H + a.hpc - 1) / a.hpc;
-  float dwa[2][4], dwb[2][4];  // queries', keys' weight gradients
+// A lane's weights and its sums of their gradient.
+struct Weights {
+  float wa[4], wb[4], dwa[4], dwb[4];
+};
+
+// One row of a lane group's token backward: its gradient at g (PARTS: in
+// parts, of head h), the forward's input at x, the output at y.
+template <int DH, bool USUAL, bool PARTS>
+__device__ __forceinline__ void rope_bwd_row(const RopeArgs& a, const RopeGrad& parts, const Lane<USUAL>& ln,
+                                             const float (&cs)[4], const float (&sn)[4], Weights& w, bool live, int h,
+                                             const float* g, const uint16_t* x, float* y) {
+  constexpr int LPT = DH / 8;
+  float4 g0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), g1 = g0;
+  uint2 x0 = make_uint2(0u, 0u), x1 = x0;
+  if (live) {
+    if constexpr (PARTS) {
+      load_parts(parts, g, h, ln, &g0, &g1);
+    } else {
+      g0 = *reinterpret_cast<const float4*>(g + 4 * ln.c0);
+      g1 = *reinterpret_cast<const float4*>(g + 4 * ln.c1);
+    }
+    if (USUAL || a.norm) {
+      x0 = *reinterpret_cast<const uint2*>(x + 4 * ln.c0);
+      x1 = *reinterpret_cast<const uint2*>(x + 4 * ln.c1);
+    }
+  }
+  float A[4], B[4];
+  to_pairs(g0, g1, ln.adjacent, A, B);
+  if (ln.rot) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwa[i / 4][i % 4] = dwb[i / 4][i % 4] = 0.0f;
-  for (long long it = blockIdx.x; it < tiles * chunks; it += gridDim.x) {
+    for (int j = 0; j < 4; ++j) {
+      const float p = A[j], q = B[j];
+      A[j] = fmaf(p, cs[j], q * sn[j]);
+      B[j] = fmaf(q, cs[j], -p * sn[j]);
+    }
+  }
+  if (USUAL || a.norm) {
+    float X[4], Y[4], s = 0.0f, gx = 0.0f;
+    unpack(x0, x1, ln.adjacent, X, Y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s = fmaf(X[j], X[j], fmaf(Y[j], Y[j], s));
+      gx = fmaf(A[j] * w.wa[j], X[j], fmaf(B[j] * w.wb[j], Y[j], gx));
+    }
+    s = lane_sum<LPT>(s);
+    gx = lane_sum<LPT>(gx);
+    // An absent row (zeros) adds nothing to the sums, eps = 0 included.
+    const float rstd = live ? rsqrtf(fmaf(s, 1.0f / DH, a.eps)) : 0.0f;
+    const float mean = gx * rstd * (1.0f / DH);  // of gw xh
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      X[j] *= rstd;
+      Y[j] *= rstd;
+      w.dwa[j] = fmaf(A[j], X[j], w.dwa[j]);
+      w.dwb[j] = fmaf(B[j], Y[j], w.dwb[j]);
+      A[j] = rstd * fmaf(-X[j], mean, A[j] * w.wa[j]);
+      B[j] = rstd * fmaf(-Y[j], mean, B[j] * w.wb[j]);
+    }
+  }
+  if (!live) return;
+  from_pairs(A, B, ln.adjacent, &g0, &g1);
+  *reinterpret_cast<float4*>(y + 4 * ln.c0) = g0;
+  *reinterpret_cast<float4*>(y + 4 * ln.c1) = g1;
+}
+
+// PARTS: the gradients come in parts (the layer's backward). CTAs below cq
+// take the queries (routed and shared), the others the keys, so that a thread
+// sums one weight gradient and keeps one set of weights.
+template <int DH, bool USUAL, bool PARTS>
+__global__ void __launch_bounds__(kThreads, kRopeBwdPerSm) rope_bwd_kernel(RopeArgs a, RopeBwdArgs d) {
+  constexpr int LPT = DH / 8, TOK = kThreads / LPT;
+  __shared__ float red[kThreads / 32][DH];
+  const Lane<USUAL> ln = lane_of<DH, USUAL>(threadIdx.x % LPT, a);
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool keys = static_cast<int>(blockIdx.x) >= d.cq;
+  const int ctas = keys ? gridDim.x - d.cq : d.cq, cta = keys ? blockIdx.x - d.cq : blockIdx.x;
+  const int H = keys ? a.n[2] : a.n[0] + a.n[1], hpc = keys ? d.hpc_k : a.hpc, chunks = (H + hpc - 1) / hpc;
+  const long long items = (a.R + TOK - 1) / TOK * chunks;
+  const float* wp = USUAL || a.norm ? (keys ? a.w_k : a.w_q) : nullptr;
+  Weights w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w.wa[j] = wp != nullptr ? __ldg(wp + ln.elem_a(j)) : 1.0f;
+    w.wb[j] = wp != nullptr ? __ldg(wp + ln.elem_b(j)) : 1.0f;
+    w.dwa[j] = w.dwb[j] = 0.0f;
+  }
+#pragma unroll 1
+  for (long long it = cta; it < items; it += ctas) {
     const long long tile = it / chunks;
-    const int first = static_cast<int>(it - tile * chunks) * a.hpc, last = first + a.hpc;
-    const long long row = tile * TOK + threadIdx.x / LPT;
+    const int first = static_cast<int>(it - tile * chunks) * hpc, last = min(first + hpc, H);
+    const int row = static_cast<int>(tile * TOK) + threadIdx.x / LPT;
     const bool on = row < a.R;
-    const int b = on ? static_cast<int>(row / a.T) : 0,
-              t = on ? static_cast<int>(row - static_cast<long long>(b) * a.T) : 0;
+    const int b = on ? row / a.T : 0, t = on ? row - b * a.T : 0;
     float cs[4], sn[4];
     angles(a, ln, on, row, b, t, cs, sn);
-    int at = 0;
-#pragma unroll
-    for (int op = 0; op < 3; ++op) {
-      constexpr int kQueries = 0, kKeys = 1;
-      const int wi = op == 2 ? kKeys : kQueries;
-      const int h0 = max(first - at, 0), h1 = min(last - at, a.n[op]);
-      at += a.n[op];
+    // The queries' routed heads, then the shared one; or the keys.
+#pragma unroll 1
+    for (int op = keys ? 2 : 0; op < (keys ? 3 : 2); ++op) {
+      const int at = op == 1 ? a.n[0] : 0, h0 = max(first - at, 0), h1 = min(last - at, a.n[op]);
       if (h0 >= h1) continue;
-      const float* w = a.norm ? (op == 2 ? a.w_k : a.w_q) : nullptr;
-      float wa[4], wb[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        wa[j] = w != nullptr ? __ldg(w + ln.elem_a(j)) : 1.0f;
-        wb[j] = w != nullptr ? __ldg(w + ln.elem_b(j)) : 1.0f;
+      const float* g = static_cast<const float*>(d.g[op].rows.p);
+      const uint16_t* x = static_cast<const uint16_t*>(a.x[op].p);
+      float* y = static_cast<float*>(a.y[op].p);
+      if (!USUAL && op == 0 && a.slot_pos != nullptr) {  // token-list order: all three at the same rows
+        for (int h = h0; h < h1; ++h) {
+          const long long o = on ? list_offset(a, row, h, DH) : -1;
+          rope_bwd_row<DH, USUAL, PARTS>(a, d.g[op], ln, cs, sn, w, o >= 0, h, g + o, x + o, y + o);
+        }
+        continue;
       }
-      auto load = [&](int h, BwdRow* r) {
-        r->off = on ? row_offset(a, a.x[op], op, row, b, t, h, DH) : -1;
-        r->g0 = r->g1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        r->x0 = r->x1 = make_uint2(0u, 0u);
-        if (r->off < 0) return;
-        const bool list = op == 0 && a.slot_pos != nullptr;
-        const float* g = static_cast<const float*>(d.g[op].rows.p) + (list ? r->off : row_offset(a, d.g[op].rows, 1, row, b, t, h, DH));
-        if constexpr (PARTS) {
-          load_parts(d.g[op], g, h, ln, &r->g0, &r->g1);
-        } else {
-          r->g0 = *reinterpret_cast<const float4*>(g + 4 * ln.c0);
-          r->g1 = *reinterpret_cast<const float4*>(g + 4 * ln.c1);
-        }
-        if (a.norm) {
-          const uint16_t* p = static_cast<const uint16_t*>(a.x[op].p) + r->off;
-          r->x0 = *reinterpret_cast<const uint2*>(p + 4 * ln.c0);
-          r->x1 = *reinterpret_cast<const uint2*>(p + 4 * ln.c1);
-        }
-      };
-      BwdRow next;
-      load(h0, &next);
-      for (int h = h0; h < h1; ++h) {
-        const BwdRow r = next;
-        if (h + 1 < h1) load(h + 1, &next);
-        float A[4], B[4];
-        to_pairs(r.g0, r.g1, ln.adjacent, A, B);
-        if (ln.rot) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = A[j], y = B[j];
-            A[j] = fmaf(x, cs[j], y * sn[j]);
-            B[j] = fmaf(y, cs[j], -x * sn[j]);
-          }
-        }
-        if (a.norm) {
-          float X[4], Y[4], s = 0.0f, gx = 0.0f;
-          unpack(r.x0, r.x1, ln.adjacent, X, Y);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s = fmaf(X[j], X[j], fmaf(Y[j], Y[j], s));
-            gx = fmaf(A[j] * wa[j], X[j], fmaf(B[j] * wb[j], Y[j], gx));
-          }
-          s = lane_sum<LPT>(s);
-          gx = lane_sum<LPT>(gx);
-          // An absent row (zeros) adds nothing to the sums, eps = 0 included.
-          const float rstd = r.off < 0 ? 0.0f : rsqrtf(fmaf(s, 1.0f / DH, a.eps));
-          const float mean = gx * rstd * (1.0f / DH);  // of gw xh
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            X[j] *= rstd;
-            Y[j] *= rstd;
-            dwa[wi][j] = fmaf(A[j], X[j], dwa[wi][j]);  // 0 where the row is absent
-            dwb[wi][j] = fmaf(B[j], Y[j], dwb[wi][j]);
-            A[j] = rstd * fmaf(-X[j], mean, A[j] * wa[j]);
-            B[j] = rstd * fmaf(-Y[j], mean, B[j] * wb[j]);
-          }
-        }
-        if (r.off < 0) continue;
-        const bool list = op == 0 && a.slot_pos != nullptr;
-        float* q = static_cast<float*>(a.y[op].p) + (list ? r.off : row_offset(a, a.y[op], 1, row, b, t, h, DH));
-        float4 o0, o1;
-        from_pairs(A, B, ln.adjacent, &o0, &o1);
-        *reinterpret_cast<float4*>(q + 4 * ln.c0) = o0;
-        *reinterpret_cast<float4*>(q + 4 * ln.c1) = o1;
-      }
+      const long long gs = d.g[op].rows.sh, xs = a.x[op].sh, ys = a.y[op].sh;
+      g += b * d.g[op].rows.sb + t * d.g[op].rows.st + h0 * gs;
+      x += b * a.x[op].sb + t * a.x[op].st + h0 * xs;
+      y += b * a.y[op].sb + t * a.y[op].st + h0 * ys;
+#pragma unroll 1
+      for (int h = h0; h < h1; ++h, g += gs, x += xs, y += ys)
+        rope_bwd_row<DH, USUAL, PARTS>(a, d.g[op], ln, cs, sn, w, on, h, g, x, y);
     }
   }
   if (d.part == nullptr) return;
-  // The weights' gradients: lanes of one column over the warp's tokens, then
+  // The weights' gradient: lanes of one column over the warp's tokens, then
   // the warps, in a fixed order; one partial row per CTA.
   const int warp = threadIdx.x / 32;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int o = LPT; o < 32; o <<= 1) {
-        dwa[i][j] += __shfl_xor_sync(0xffffffffu, dwa[i][j], o);
-        dwb[i][j] += __shfl_xor_sync(0xffffffffu, dwb[i][j], o);
-      }
-      if (threadIdx.x % 32 < LPT) {
-        red[warp][i][ln.elem_a(j)] = dwa[i][j];
-        red[warp][i][ln.elem_b(j)] = dwb[i][j];
-      }
+    for (int o = LPT; o < 32; o <<= 1) {
+      w.dwa[j] += __shfl_xor_sync(0xffffffffu, w.dwa[j], o);
+      w.dwb[j] += __shfl_xor_sync(0xffffffffu, w.dwb[j], o);
     }
+    if (threadIdx.x % 32 < LPT) {
+      red[warp][ln.elem_a(j)] = w.dwa[j];
+      red[warp][ln.elem_b(j)] = w.dwb[j];
+    }
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * DH; i += kThreads) {
+  for (int i = threadIdx.x; i < DH; i += kThreads) {
     float s = 0.0f;
 #pragma unroll
-    for (int wp = 0; wp < kThreads / 32; ++wp) s += red[wp][i / DH][i % DH];
-    d.part[static_cast<size_t>(blockIdx.x) * 2 * DH + i] = s;
+    for (int wi = 0; wi < kThreads / 32; ++wi) s += red[wi][i];
+    d.part[static_cast<size_t>(blockIdx.x) * DH + i] = s;
   }
 }
 
-// dw[j] = sum over the CTAs' partials, one block per 4 columns, fixed order.
+// dw[j] = sum over the CTAs' partials (rows below cq: the queries', then the
+// keys'), one block per 4 columns, fixed order.
 template <int DH>
-__global__ void __launch_bounds__(kThreads) rope_dw_kernel(const float* part, int n, float* dw_q, float* dw_k) {
+__global__ void __launch_bounds__(kThreads) rope_dw_kernel(const float* part, int cq, int n, float* dw_q, float* dw_k) {
   __shared__ float4 red[kThreads];
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool keys = blockIdx.x >= DH / 4;
+  const int col = 4 * (blockIdx.x % (DH / 4));
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float4 v = *reinterpret_cast<const float4*>(part + static_cast<size_t>(i) * 2 * DH + 4 * blockIdx.x);
+  for (int i = threadIdx.x + (keys ? cq : 0); i < (keys ? n : cq); i += kThreads) {
+    const float4 v = *reinterpret_cast<const float4*>(part + static_cast<size_t>(i) * DH + col);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
   red[threadIdx.x] = s;
@@ -402,11 +440,8 @@ __global__ void __launch_bounds__(kThreads) rope_dw_kernel(const float* part, in
     }
     __syncthreads();
   }
-  if (threadIdx.x < 4) {
-    const int col = 4 * blockIdx.x + threadIdx.x;
-    float* dw = col < DH ? dw_q : dw_k;
-    if (dw != nullptr) dw[col % DH] = reinterpret_cast<const float*>(red)[threadIdx.x];
-  }
+  float* dw = keys ? dw_k : dw_q;
+  if (threadIdx.x < 4 && dw != nullptr) dw[col + threadIdx.x] = reinterpret_cast<const float*>(red)[threadIdx.x];
 }
 
 }  // namespace rope_impl
@@ -420,34 +455,50 @@ static int heads_per_cta(long long tiles, int H) {
   return static_cast<int>((H + chunks - 1) / chunks);
 }
 
+static bool usual(const RopeArgs& a, int dh) { return a.norm && !a.adjacent && a.d_rot == dh && a.slot_pos == nullptr; }
+
 int rope_fwd(RopeArgs a, int dh, void* stream) {
   const int tok = rope_impl::kThreads / (dh / 8), H = a.n[0] + a.n[1] + a.n[2];
   const long long tiles = (a.R + tok - 1) / tok;
   a.hpc = heads_per_cta(tiles, H);
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((H + a.hpc - 1) / a.hpc));
-  return dh == 64 ? launch_pdl(rope_kernel<64>, grid, dim3(rope_impl::kThreads), 0, stream, a)
-                  : launch_pdl(rope_kernel<32>, grid, dim3(rope_impl::kThreads), 0, stream, a);
+  auto kernel = dh == 64 ? (usual(a, dh) ? rope_kernel<64, true> : rope_kernel<64, false>)
+                         : (usual(a, dh) ? rope_kernel<32, true> : rope_kernel<32, false>);
+  return launch_pdl(kernel, grid, dim3(rope_impl::kThreads), 0, stream, a);
 }
 
-size_t rope_bwd_ws_bytes(int dh) { return static_cast<size_t>(kRopeCtas) * 2 * dh * sizeof(float); }
+size_t rope_bwd_ws_bytes(int dh) { return static_cast<size_t>(kRopeBwdCtas) * dh * sizeof(float); }
 
-int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* ws, void* stream) {
-  const int tok = rope_impl::kThreads / (dh / 8), H = a.n[0] + a.n[1] + a.n[2];
-  const long long tiles = (a.R + tok - 1) / tok;
-  a.hpc = heads_per_cta(tiles, H);
-  const long long items = tiles * ((H + a.hpc - 1) / a.hpc);
-  const int ctas = static_cast<int>(items < kRopeCtas ? items : kRopeCtas);
-  const bool dw = a.norm && (dw_q != nullptr || dw_k != nullptr);
-  d.part = dw ? static_cast<float*>(ws) : nullptr;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+template <int DH>
+static int launch_bwd(const RopeArgs& a, const RopeBwdArgs& d, int ctas, float* dw_q, float* dw_k, void* stream) {
   bool parts = false;
   for (int i = 0; i < 3; ++i) parts = parts || d.g[i].parts * d.g[i].streams != 1 || d.g[i].extra != 0;
-  auto kernel = dh == 64 ? (parts ? rope_bwd_kernel<64, true> : rope_bwd_kernel<64, false>)
-                         : (parts ? rope_bwd_kernel<32, true> : rope_bwd_kernel<32, false>);
-  kernel<<<ctas, rope_impl::kThreads, 0, st>>>(a, d);
-  if (dw && dh == 64) rope_dw_kernel<64><<<2 * 64 / 4, rope_impl::kThreads, 0, st>>>(d.part, ctas, dw_q, dw_k);
-  if (dw && dh == 32) rope_dw_kernel<32><<<2 * 32 / 4, rope_impl::kThreads, 0, st>>>(d.part, ctas, dw_q, dw_k);
-  return cudaGetLastError();
+  auto kernel = parts ? rope_bwd_kernel<DH, false, true>
+                      : (usual(a, DH) ? rope_bwd_kernel<DH, true, false> : rope_bwd_kernel<DH, false, false>);
+  int e = launch_pdl(kernel, dim3(ctas), dim3(rope_impl::kThreads), 0, stream, a, d);
+  if (e == cudaSuccess && d.part != nullptr)
+    e = launch_pdl(rope_dw_kernel<DH>, dim3(2 * DH / 4), dim3(rope_impl::kThreads), 0, stream,
+                   static_cast<const float*>(d.part), d.cq, ctas, dw_q, dw_k);
+  return e;
+}
+
+int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* ws, void* stream) {
+  const int tok = rope_impl::kThreads / (dh / 8), Hq = a.n[0] + a.n[1], Hk = a.n[2];
+  const long long tiles = (a.R + tok - 1) / tok;
+  // Runs of heads of about one length in both classes.
+  const int hpc = heads_per_cta(tiles, Hq + Hk);
+  const int nq = (Hq + hpc - 1) / hpc, nk = (Hk + hpc - 1) / hpc;
+  a.hpc = nq > 0 ? (Hq + nq - 1) / nq : 1;
+  d.hpc_k = nk > 0 ? (Hk + nk - 1) / nk : 1;
+  const long long items = tiles * (nq + nk);
+  const int ctas = static_cast<int>(items < kRopeBwdCtas ? items : kRopeBwdCtas);
+  // Resident CTAs shared out by the classes' rows, at least one for each.
+  int cq = (ctas * Hq + (Hq + Hk) / 2) / (Hq + Hk);
+  if (Hq > 0 && cq == 0) cq = 1;
+  if (Hk > 0 && cq == ctas) cq = ctas > 1 ? ctas - 1 : 0;
+  d.cq = cq;
+  d.part = a.norm && (dw_q != nullptr || dw_k != nullptr) ? static_cast<float*>(ws) : nullptr;
+  return dh == 64 ? launch_bwd<64>(a, d, ctas, dw_q, dw_k, stream) : launch_bwd<32>(a, d, ctas, dw_q, dw_k, stream);
 }
 
 }  // namespace gqe
