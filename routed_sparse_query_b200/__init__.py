@@ -58,20 +58,40 @@ class GQEConfig(ctypes.Structure):
         return cls(shape.B, shape.T, shape.d_model, shape.G, shape.M, shape.k, shape.d_head, flags)
 
 
+# torch's own cheap accessors where it has them (a Stream object costs 3 us to make).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _first_device(*tensors) -> int:
+    """The CUDA device of the first tensor given (of none: the current one)."""
+    for t in tensors:
+        if t is not None:
+            dev = t.get_device()
+            if dev < 0:
+                raise ValueError("tensors must be contiguous CUDA tensors")
+            return dev
+    return _current_device()
+
+
 def _arg(t, dtype, n, dev, name):
     """Pointer of an optional argument: contiguous, on CUDA device `dev`, of the
     given type and (n not None) element count."""
     if t is None:
         return None
+    if t.get_device() != dev or t.dtype is not dtype or (n is not None and t.numel() != n) or not t.is_contiguous():
+        _refuse(t, dtype, n, dev, name)
+    return t.data_ptr()
+
+
+def _refuse(t, dtype, n, dev, name):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: tensors must be contiguous CUDA tensors")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors on cuda:{dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name}: {t.numel()} elements, {n} are needed")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {t.numel()} elements, {n} are needed")
 
 
 class GQERope(ctypes.Structure):
@@ -93,7 +113,7 @@ class GQERope(ctypes.Structure):
         tensors = [(pos, torch.int32, None, "pos"), (inv_freq, torch.float64, half, "inv_freq"),
                    (axis, torch.int32, half, "axis"), (w_q, torch.float32, None, "w_q"), (w_k, torch.float32, None, "w_k")]
         given = [t for t, _, _, _ in tensors if t is not None]
-        dev = given[0].get_device() if given else -1
+        dev = _first_device(*given) if given else -1
         self = cls(d_rot, axes, flags, eps, scale, *(_arg(t, d, n, dev, what) for t, d, n, what in tensors))
         self._refs, self._dev = given, dev
         self._n_pos = None if pos is None else pos.numel()
@@ -113,7 +133,7 @@ class GQEKv4(ctypes.Structure):
         if k_codes.dim() != 4:
             raise ValueError("k_codes is [B, G, capacity, d_head/2]")
         B, G, cap, half = k_codes.shape
-        dev = k_codes.get_device()
+        dev = _first_device(k_codes)
         self = cls(_arg(k_codes, torch.uint8, None, dev, "k_codes"),
                    _arg(v_codes, torch.uint8, k_codes.numel(), dev, "v_codes"),
                    _arg(meta, torch.bfloat16, B * G * cap * 4, dev, "meta"), cap)
@@ -129,7 +149,7 @@ class GQEBalance(ctypes.Structure):
 
     @classmethod
     def of(cls, counts, sums, loss=None, mask=None, c_balance: float = 0.0, c_z: float = 0.0) -> "GQEBalance":
-        dev = counts.get_device()
+        dev = _first_device(counts)
         self = cls(_arg(mask, torch.uint8, None, dev, "mask"), c_balance, c_z,
                    _arg(counts, torch.int32, None, dev, "counts"), _arg(sums, torch.float32, counts.numel(), dev, "sums"),
                    _arg(loss, torch.float32, 3, dev, "loss"))
@@ -203,9 +223,7 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -313,25 +331,17 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 def _call(name, dev, stream, *args):
     """The C entry point on device `dev` and on `stream` (default: that device's
     current stream)."""
-    fn = getattr(_lib, name)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            status = fn(*args, _stream(stream))
+    if dev == _current_device():
+        status = getattr(_lib, name)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
-        status = fn(*args, _stream(stream))
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, _stream(stream))
     if status != GQE_OK:
         raise GQEError(status, name)
 
 
 def _config(cfg) -> GQEConfig:
     return cfg if isinstance(cfg, GQEConfig) else GQEConfig.of(cfg)
-
-
-def _first_device(*tensors) -> int:
-    for t in tensors:
-        if t is not None:
-            return t.get_device()
-    return torch.cuda.current_device()
 
 
 def _ws(ws, dev):

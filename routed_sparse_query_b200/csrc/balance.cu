@@ -29,6 +29,7 @@ namespace balance_impl {
 
 constexpr int kThreads = 256;
 constexpr int kMaxCtas = 148 * 4;
+constexpr int kAhead = 4;  // rows of a thread in flight
 
 struct BalanceArgs {
   const float* z;       // [R, G M]
@@ -39,38 +40,56 @@ struct BalanceArgs {
   float* part;          // [CTAs][2 N + 2]: counts (as int bits), sum p, sum lse^2, rows (int bits)
 };
 
-template <int LANES, int PER>
-struct Pair {
-  float z[PER], p[PER];
-  float lse;
-  // Softmax of the pair's logits; lane q holds experts q, q + LANES, ...
-  // `live` lanes only; the others join the exchanges.
-  __device__ __forceinline__ void load(const float* zp, int q, int M, bool live) {
-    float m = -INFINITY;
+// Logits of one (row, group) pair: lane q holds experts q, q + LANES, ...
+// EXACT: M = PER in one lane, read in one piece.
+template <int LANES, int PER, bool EXACT>
+__device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool at, float (&z)[PER]) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int j = q + i * LANES;
-      z[i] = live && j < M ? __ldg(zp + j) : -INFINITY;
-      m = fmaxf(m, z[i]);
+  for (int i = 0; i < PER; ++i) z[i] = -INFINITY;
+  if (!at) return;
+  if constexpr (EXACT && PER % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(zp + i));
+      z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
     }
+  } else if constexpr (EXACT && PER == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(zp));
+    z[0] = v.x; z[1] = v.y;
+  } else {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      p[i] = live && q + i * LANES < M ? expf(z[i] - m) : 0.0f;
-      s += p[i];
-    }
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) p[i] = live ? p[i] / s : 0.0f;
-    lse = live ? m + logf(s) : 0.0f;
+    for (int i = 0; i < PER; ++i)
+      if (q + i * LANES < M) z[i] = __ldg(zp + q + i * LANES);
   }
-};
+}
 
-// Threads of a CTA: `rows` rows x G groups x LANES lanes (the rest idle).
+// z to probabilities; the log of the sum of exp. exp and log are the fast
+// ones (2^-21 of the result near 1, 2^-19 for e^-20): far inside what fp32
+// sums over the rows keep.
 template <int LANES, int PER>
+__device__ __forceinline__ float softmax(float (&z)[PER]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    z[i] = __expf(z[i] - m);
+    s += z[i];
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float inv = __fdividef(1.0f, s);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) z[i] *= inv;
+  return m + __logf(s);
+}
+
+// Threads of a CTA: `rows` rows x G groups x LANES lanes (the rest idle),
+// kAhead rows of each thread in flight.
+template <int LANES, int PER, bool EXACT>
 __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
   __shared__ float sp[kThreads * PER];
   __shared__ int sc[kThreads * PER];
@@ -81,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
   const int gl = a.G * LANES, rows = kThreads / gl;
   const int tid = threadIdx.x, rl = tid / gl, g = (tid % gl) / LANES, q = tid % LANES;
   const bool in = rl < rows;
+  const long long step = static_cast<long long>(gridDim.x) * rows;
   float psum[PER], lsum = 0.0f;
   int cnt[PER], n = 0;
 #pragma unroll
@@ -88,21 +108,44 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
     psum[i] = 0.0f;
     cnt[i] = 0;
   }
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += static_cast<long long>(gridDim.x) * rows) {
-    const long long r = r0 + rl;
-    const bool live = in && r < a.R && (a.mask == nullptr || a.mask[r] != 0);
-    Pair<LANES, PER> w;
-    w.load(a.z + (r * a.G + g) * a.M, q, a.M, live);
-    if (live) {
+  auto count = [&](int j, bool live) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) psum[i] += w.p[i];
-      for (int s = 0; s < a.k; ++s) {
-        const int j = __ldg(a.idx + (r * a.G + g) * a.k + s);
+    for (int i = 0; i < PER; ++i) cnt[i] += live && j == q + i * LANES ? 1 : 0;
+  };
+  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += kAhead * step) {
+    float z[kAhead][PER];
+    bool live[kAhead];
+    int sel[kAhead][2];  // the first two selections (k <= 2 is the usual case)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) cnt[i] += j == q + i * LANES ? 1 : 0;
+    for (int u = 0; u < kAhead; ++u) {
+      const long long r = r0 + u * step + rl;
+      const bool at = in && r < a.R;
+      load_logits<LANES, PER, EXACT>(a.z + (r * a.G + g) * a.M, q, a.M, at, z[u]);
+      live[u] = at && (a.mask == nullptr || a.mask[r] != 0);
+      const int32_t* ip = a.idx + (r * a.G + g) * a.k;
+      sel[u][0] = sel[u][1] = -1;
+      if (at && a.k == 2) {
+        const int2 v = __ldg(reinterpret_cast<const int2*>(ip));
+        sel[u][0] = v.x;
+        sel[u][1] = v.y;
+      } else if (at && a.k == 1) {
+        sel[u][0] = __ldg(ip);
       }
-      if (q == 0) lsum = fmaf(w.lse, w.lse, lsum);
-      if (g == 0 && q == 0) ++n;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float lse = softmax<LANES, PER>(z[u]);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) psum[i] += live[u] ? z[u][i] : 0.0f;
+      if (a.k <= 2) {
+        count(sel[u][0], live[u]);
+        count(sel[u][1], live[u]);
+      } else if (live[u]) {
+        const int32_t* ip = a.idx + ((r0 + u * step + rl) * a.G + g) * a.k;
+        for (int s = 0; s < a.k; ++s) count(__ldg(ip + s), true);
+      }
+      if (live[u] && q == 0) lsum = fmaf(lse, lse, lsum);
+      if (live[u] && q == 0 && g == 0) ++n;
     }
   }
 #pragma unroll
@@ -127,40 +170,49 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
     out[e] = __int_as_float(c);
     out[N + e] = s;
   }
-  if (tid == kThreads - 1) {
+  if (tid >= kThreads - 32) {  // the last warp: the two sums over all threads
     float s = 0.0f;
     int c = 0;
-    for (int i = 0; i < kThreads; ++i) {
+    for (int i = tid & 31; i < kThreads; i += 32) {
       s += sl[i];
       c += sn[i];
     }
-    out[2 * N] = s;
-    out[2 * N + 1] = __int_as_float(c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
+    if (tid == kThreads - 1) {
+      out[2 * N] = s;
+      out[2 * N + 1] = __int_as_float(c);
+    }
   }
 }
 
-// One CTA: the sums over the stats CTAs. 8 lanes per column.
+// One CTA: the sums over the stats CTAs; neighbouring threads on neighbouring
+// columns, as many rows at a time as there are threads for.
 __global__ void __launch_bounds__(1024) finish_kernel(const float* part, int ctas, int N, int32_t* counts, float* sums) {
+  __shared__ double acc[1024];
   pdl_wait();
   pdl_launch_dependents();
-  const int cols = 2 * N + 2, q = threadIdx.x % 8;
-  for (int c0 = 0; c0 < cols; c0 += 128) {
-    const int col = c0 + threadIdx.x / 8;
-    const bool whole = col < N || col == 2 * N + 1;
-    double s = 0.0;
-    if (col < cols)
-      for (int i = q; i < ctas; i += 8) {
-        const float v = part[static_cast<size_t>(i) * cols + col];
-        s += whole ? static_cast<double>(__float_as_int(v)) : static_cast<double>(v);
-      }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (q == 0 && col < cols) {
-      if (col < N) counts[col] = static_cast<int32_t>(s);
-      else if (col <= 2 * N) sums[col - N] = static_cast<float>(s);
-      else counts[N] = static_cast<int32_t>(s);
+  const int cols = 2 * N + 2, wide = (cols + 31) / 32 * 32, groups = 1024 / wide;
+  const int col = threadIdx.x % wide, grp = threadIdx.x / wide;
+  const bool whole = col < N || col == 2 * N + 1;
+  double s = 0.0;
+  if (col < cols && grp < groups) {
+#pragma unroll 8
+    for (int i = grp; i < ctas; i += groups) {
+      const float v = part[static_cast<size_t>(i) * cols + col];
+      s += whole ? static_cast<double>(__float_as_int(v)) : static_cast<double>(v);
     }
   }
+  acc[threadIdx.x] = s;
+  __syncthreads();
+  if (grp != 0 || col >= cols) return;
+  for (int i = 1; i < groups; ++i) s += acc[i * wide + col];
+  if (col < N) counts[col] = static_cast<int32_t>(s);
+  else if (col <= 2 * N) sums[col - N] = static_cast<float>(s);
+  else counts[N] = static_cast<int32_t>(s);
 }
 
 struct GradArgs {
@@ -176,7 +228,7 @@ struct GradArgs {
   int accumulate;
 };
 
-template <int LANES, int PER>
+template <int LANES, int PER, bool EXACT>
 __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -210,39 +262,77 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs a) {
   }
   const float cb = static_cast<float>(static_cast<double>(a.c_balance) * a.M / (a.G * n));
   const float cz = static_cast<float>(2.0 * a.c_z / (a.G * n));
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += static_cast<long long>(gridDim.x) * rows) {
-    const long long r = r0 + rl;
-    const bool at = in && r < a.R;
-    const bool live = at && (a.mask == nullptr || a.mask[r] != 0);
-    Pair<LANES, PER> w;
-    w.load(a.z + (r * a.G + g) * a.M, q, a.M, live);
-    float mean = 0.0f;
+  const long long step = static_cast<long long>(gridDim.x) * rows;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += kAhead * step) {
+    float z[kAhead][PER];
+    bool at[kAhead], live[kAhead];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mean = fmaf(w.p[i], f[i], mean);
+    for (int u = 0; u < kAhead; ++u) {
+      const long long r = r0 + u * step + rl;
+      at[u] = in && r < a.R;
+      load_logits<LANES, PER, EXACT>(a.z + (r * a.G + g) * a.M, q, a.M, at[u], z[u]);
+      live[u] = at[u] && (a.mask == nullptr || a.mask[r] != 0);
+    }
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-    float* out = a.dz + (r * a.G + g) * a.M;
+    for (int u = 0; u < kAhead; ++u) {
+      const float lse = softmax<LANES, PER>(z[u]);
+      float mean = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int j = q + i * LANES;
-      if (!at || j >= a.M) continue;
-      const float d = live ? w.p[i] * (cb * (f[i] - mean) + cz * w.lse) : 0.0f;
-      if (!a.accumulate) out[j] = d;
-      else if (live) out[j] += d;
+      for (int i = 0; i < PER; ++i) mean = fmaf(z[u][i], f[i], mean);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) z[u][i] = live[u] ? z[u][i] * (cb * (f[i] - mean) + cz * lse) : 0.0f;
+      if (!at[u]) continue;
+      float* out = a.dz + ((r0 + u * step + rl) * a.G + g) * a.M;
+      if constexpr (EXACT && PER % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+          float4* o = reinterpret_cast<float4*>(out + i);
+          float4 v = make_float4(z[u][i], z[u][i + 1], z[u][i + 2], z[u][i + 3]);
+          if (a.accumulate) {
+            const float4 w = *o;
+            v = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
+          }
+          *o = v;
+        }
+      } else if constexpr (EXACT && PER == 2) {
+        float2* o = reinterpret_cast<float2*>(out);
+        float2 v = make_float2(z[u][0], z[u][1]);
+        if (a.accumulate) {
+          const float2 w = *o;
+          v = make_float2(w.x + v.x, w.y + v.y);
+        }
+        *o = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int j = q + i * LANES;
+          if (j < a.M) out[j] = a.accumulate ? out[j] + z[u][i] : z[u][i];
+        }
+      }
     }
   }
 }
 
-// Instantiation for M: up to 8 logits in one lane, more on 8 lanes.
+// Instantiation for M: up to 8 logits in one lane (1, 2, 4 and 8 in one
+// piece), more on 8 lanes.
+template <int L, int P, bool E>
+struct Shape {
+  static constexpr int LANES = L, PER = P;
+  static constexpr bool EXACT = E;
+};
 template <typename F>
 int with_shape(int M, F f) {
-  if (M <= 1) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (M <= 2) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-  if (M <= 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  if (M <= 8) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-  if (M <= 16) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-  if (M <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  if (M == 1) return f(Shape<1, 1, true>{});
+  if (M == 2) return f(Shape<1, 2, true>{});
+  if (M == 4) return f(Shape<1, 4, true>{});
+  if (M == 8) return f(Shape<1, 8, true>{});
+  if (M < 4) return f(Shape<1, 4, false>{});
+  if (M < 8) return f(Shape<1, 8, false>{});
+  if (M <= 16) return f(Shape<8, 2, false>{});
+  if (M <= 32) return f(Shape<8, 4, false>{});
+  return f(Shape<8, 8, false>{});
 }
 
 int ctas_for(long long R, int G, int M) {
@@ -260,8 +350,9 @@ int balance_stats(const float* z, const int32_t* idx, const uint8_t* mask, long 
                   int32_t* counts, float* sums, void* ws, void* stream) {
   const BalanceArgs a{z, idx, mask, R, G, M, k, static_cast<float*>(ws)};
   const int ctas = ctas_for(R, G, M);
-  const int e = with_shape(M, [&](auto lanes, auto per) {
-    return static_cast<int>(launch_pdl(stats_kernel<decltype(lanes)::value, decltype(per)::value>, dim3(ctas),
+  const int e = with_shape(M, [&](auto s) {
+    using S = decltype(s);
+    return static_cast<int>(launch_pdl(stats_kernel<S::LANES, S::PER, S::EXACT>, dim3(ctas),
                                        dim3(balance_impl::kThreads), 0, stream, a));
   });
   if (e != cudaSuccess) return e;
@@ -273,8 +364,9 @@ int balance_grad(const float* z, const uint8_t* mask, const int32_t* counts, con
                  int M, int k, float c_balance, float c_z, float* loss, float* dz, bool accumulate, void* stream) {
   const GradArgs a{z, mask, counts, sums, R, G, M, k, c_balance, c_z, loss, dz, accumulate ? 1 : 0};
   const int ctas = dz != nullptr ? ctas_for(R, G, M) : 1;
-  return with_shape(M, [&](auto lanes, auto per) {
-    return static_cast<int>(launch_pdl(grad_kernel<decltype(lanes)::value, decltype(per)::value>, dim3(ctas),
+  return with_shape(M, [&](auto s) {
+    using S = decltype(s);
+    return static_cast<int>(launch_pdl(grad_kernel<S::LANES, S::PER, S::EXACT>, dim3(ctas),
                                        dim3(balance_impl::kThreads), 0, stream, a));
   });
 }
