@@ -28,7 +28,7 @@ namespace gqe {
 namespace balance_impl {
 
 constexpr int kThreads = 256;
-constexpr int kMaxCtas = 148 * 4;
+constexpr int kMaxCtas = 148 * 5;
 constexpr int kAhead = 4;  // rows of a thread in flight
 
 struct BalanceArgs {
@@ -90,7 +90,7 @@ __device__ __forceinline__ float softmax(float (&z)[PER]) {
 // Threads of a CTA: `rows` rows x G groups x LANES lanes (the rest idle),
 // kAhead rows of each thread in flight.
 template <int LANES, int PER, bool EXACT>
-__global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(BalanceArgs a) {
   __shared__ float sp[kThreads * PER];
   __shared__ int sc[kThreads * PER];
   __shared__ float sl[kThreads];
@@ -112,17 +112,20 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) cnt[i] += live && j == q + i * LANES ? 1 : 0;
   };
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += kAhead * step) {
+  const long long zs = step * a.G * a.M, is = step * a.G * a.k;
+  long long r = static_cast<long long>(blockIdx.x) * rows + rl;
+  const float* zp = a.z + (r * a.G + g) * a.M;
+  const int32_t* ip0 = a.idx + (r * a.G + g) * a.k;
+  for (long long r0 = r - rl; r0 < a.R; r0 += kAhead * step, r += kAhead * step, zp += kAhead * zs, ip0 += kAhead * is) {
     float z[kAhead][PER];
     bool live[kAhead];
     int sel[kAhead][2];  // the first two selections (k <= 2 is the usual case)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const long long r = r0 + u * step + rl;
-      const bool at = in && r < a.R;
-      load_logits<LANES, PER, EXACT>(a.z + (r * a.G + g) * a.M, q, a.M, at, z[u]);
-      live[u] = at && (a.mask == nullptr || a.mask[r] != 0);
-      const int32_t* ip = a.idx + (r * a.G + g) * a.k;
+      const bool at = in && r + u * step < a.R;
+      load_logits<LANES, PER, EXACT>(zp + u * zs, q, a.M, at, z[u]);
+      live[u] = at && (a.mask == nullptr || a.mask[r + u * step] != 0);
+      const int32_t* ip = ip0 + u * is;
       sel[u][0] = sel[u][1] = -1;
       if (at && a.k == 2) {
         const int2 v = __ldg(reinterpret_cast<const int2*>(ip));
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
         count(sel[u][0], live[u]);
         count(sel[u][1], live[u]);
       } else if (live[u]) {
-        const int32_t* ip = a.idx + ((r0 + u * step + rl) * a.G + g) * a.k;
+        const int32_t* ip = ip0 + u * is;
         for (int s = 0; s < a.k; ++s) count(__ldg(ip + s), true);
       }
       if (live[u] && q == 0) lsum = fmaf(lse, lse, lsum);
@@ -189,27 +192,27 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(BalanceArgs a) {
   }
 }
 
-// One CTA: the sums over the stats CTAs; neighbouring threads on neighbouring
-// columns, as many rows at a time as there are threads for.
-__global__ void __launch_bounds__(1024) finish_kernel(const float* part, int ctas, int N, int32_t* counts, float* sums) {
-  __shared__ double acc[1024];
+// The sums over the stats CTAs, 8 columns (32 bytes of a row) per CTA.
+__global__ void __launch_bounds__(kThreads) finish_kernel(const float* part, int ctas, int N, int32_t* counts, float* sums) {
+  __shared__ double acc[kThreads / 32][8];
   pdl_wait();
   pdl_launch_dependents();
-  const int cols = 2 * N + 2, wide = (cols + 31) / 32 * 32, groups = 1024 / wide;
-  const int col = threadIdx.x % wide, grp = threadIdx.x / wide;
+  const int cols = 2 * N + 2, col = blockIdx.x * 8 + threadIdx.x % 8;
   const bool whole = col < N || col == 2 * N + 1;
   double s = 0.0;
-  if (col < cols && grp < groups) {
+  if (col < cols) {
 #pragma unroll 8
-    for (int i = grp; i < ctas; i += groups) {
+    for (int i = threadIdx.x / 8; i < ctas; i += kThreads / 8) {
       const float v = part[static_cast<size_t>(i) * cols + col];
       s += whole ? static_cast<double>(__float_as_int(v)) : static_cast<double>(v);
     }
   }
-  acc[threadIdx.x] = s;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if (threadIdx.x % 32 < 8) acc[threadIdx.x / 32][threadIdx.x % 8] = s;
   __syncthreads();
-  if (grp != 0 || col >= cols) return;
-  for (int i = 1; i < groups; ++i) s += acc[i * wide + col];
+  if (threadIdx.x >= 8 || col >= cols) return;
+  for (int i = 1; i < kThreads / 32; ++i) s += acc[i][threadIdx.x];
   if (col < N) counts[col] = static_cast<int32_t>(s);
   else if (col <= 2 * N) sums[col - N] = static_cast<float>(s);
   else counts[N] = static_cast<int32_t>(s);
@@ -229,7 +232,7 @@ struct GradArgs {
 };
 
 template <int LANES, int PER, bool EXACT>
-__global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs a) {
+__global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) grad_kernel(GradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int N = a.G * a.M, tid = threadIdx.x;
@@ -263,15 +266,16 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs a) {
   const float cb = static_cast<float>(static_cast<double>(a.c_balance) * a.M / (a.G * n));
   const float cz = static_cast<float>(2.0 * a.c_z / (a.G * n));
   const long long step = static_cast<long long>(gridDim.x) * rows;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * rows; r0 < a.R; r0 += kAhead * step) {
+  const long long zs = step * a.G * a.M;
+  long long r = static_cast<long long>(blockIdx.x) * rows + rl, at0 = (r * a.G + g) * a.M;
+  for (long long r0 = r - rl; r0 < a.R; r0 += kAhead * step, r += kAhead * step, at0 += kAhead * zs) {
     float z[kAhead][PER];
     bool at[kAhead], live[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const long long r = r0 + u * step + rl;
-      at[u] = in && r < a.R;
-      load_logits<LANES, PER, EXACT>(a.z + (r * a.G + g) * a.M, q, a.M, at[u], z[u]);
-      live[u] = at[u] && (a.mask == nullptr || a.mask[r] != 0);
+      at[u] = in && r + u * step < a.R;
+      load_logits<LANES, PER, EXACT>(a.z + at0 + u * zs, q, a.M, at[u], z[u]);
+      live[u] = at[u] && (a.mask == nullptr || a.mask[r + u * step] != 0);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs a) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) z[u][i] = live[u] ? z[u][i] * (cb * (f[i] - mean) + cz * lse) : 0.0f;
       if (!at[u]) continue;
-      float* out = a.dz + ((r0 + u * step + rl) * a.G + g) * a.M;
+      float* out = a.dz + at0 + u * zs;
       if constexpr (EXACT && PER % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
@@ -356,7 +360,7 @@ int balance_stats(const float* z, const int32_t* idx, const uint8_t* mask, long 
                                        dim3(balance_impl::kThreads), 0, stream, a));
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(finish_kernel, dim3(1), dim3(1024), 0, stream, static_cast<const float*>(a.part), ctas, G * M,
+  return launch_pdl(finish_kernel, dim3((2 * G * M + 2 + 7) / 8), dim3(balance_impl::kThreads), 0, stream, static_cast<const float*>(a.part), ctas, G * M,
                     counts, sums);
 }
 

@@ -25,6 +25,7 @@ namespace kv4_impl {
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ float bf16_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ __nv_bfloat162 bf162(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 
 struct StoreArgs {
   const uint16_t* K;   // [B][G][T][dh]
@@ -38,10 +39,12 @@ struct StoreArgs {
   int B, G, T;
 };
 
-// Cache row of (b, g, t), or -1: t is past the sequence's count, or the
-// position is outside the cache (recorded, unless it is before position 0).
-__device__ __forceinline__ long long cache_row(const StoreArgs& a, long long bg, int t) {
-  const int b = static_cast<int>(bg / a.G);
+// Cache row of row r = (b G + g) T + t (fewer than 2^31), or -1: t is past the
+// sequence's count, or the position is outside the cache (recorded, unless it
+// is before position 0).
+__device__ __forceinline__ long long cache_row(const StoreArgs& a, uint32_t r) {
+  const uint32_t bg = r / static_cast<uint32_t>(a.T), b = bg / static_cast<uint32_t>(a.G);
+  const int t = static_cast<int>(r - bg * a.T);
   if (a.count != nullptr && t >= a.count[b]) return -1;
   const long long p = static_cast<long long>(a.start != nullptr ? a.start[b] : a.start0) + t;
   if (p < 0) return -1;
@@ -49,30 +52,43 @@ __device__ __forceinline__ long long cache_row(const StoreArgs& a, long long bg,
     set_status(GQE_ERR_DEVICE_CHECK);
     return -1;
   }
-  return bg * a.c.capacity + p;
+  return static_cast<long long>(bg) * a.c.capacity + p;
 }
 
 // This lane's 8 codes of a row, and the row's (scale, zero) word.
+//
+// The quotient (x - zero) / scale is needed to the nearest whole number only:
+// a product with the approximate reciprocal is within 2^-17 of it, so that
+// quotients further than 2^-16 from a half are settled. Of the others nearly
+// all are halves exactly (values and scales have 8 bits), which an exact
+// remainder shows; what is left (and scales whose reciprocal leaves fp32)
+// takes the definition's division. Adding 1.5 * 2^23 rounds to a whole number,
+// half to even.
 template <int LPR>
 __device__ __forceinline__ uint32_t quantise(uint4 raw, uint32_t* meta) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  constexpr float kRound = 12582912.0f;
   float x[8];
-  float lo = INFINITY, hi = -INFINITY;
-  bool bad = false;
+  float zero_if_finite = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    bad = bad || !(fabsf(x[i]) < INFINITY);
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
+    zero_if_finite = fmaf(x[i], 0.0f, zero_if_finite);
+  }
+  __nv_bfloat162 lo2 = bf162(w[0]), hi2 = lo2;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    lo2 = __hmin2(lo2, bf162(w[i]));
+    hi2 = __hmax2(hi2, bf162(w[i]));
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo2 = __hmin2(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+    hi2 = __hmax2(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
   }
+  const float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
   const uint32_t group = ((1u << LPR) - 1u) << (threadIdx.x % 32 / LPR * LPR);
-  if ((__ballot_sync(0xffffffffu, bad) & group) != 0u) {
+  if ((__ballot_sync(0xffffffffu, zero_if_finite != 0.0f) & group) != 0u) {  // NaN != 0
     *meta = 0x7fff7fffu;
     return 0u;
   }
@@ -81,65 +97,113 @@ __device__ __forceinline__ uint32_t quantise(uint4 raw, uint32_t* meta) {
   const uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(0.5f * hi - 0.5f * lo, 7.5f)));
   const float s = bf16_f(sb), hs = 0.5f * s, hz = 0.5f * lo;
   *meta = sb | (__float_as_uint(lo) & 0xffff0000u);
-  uint32_t codes = 0u;
+  if (!(s > 0.0f)) return 0u;
+  const float inv = __fdividef(1.0f, hs);
+  bool settled = true;
+  float n[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(0.5f * x[i] - hz, hs)), 0.0f), 15.0f) : 0.0f;
-    codes |= static_cast<uint32_t>(q) << (4 * i);
+    const float q = (0.5f * x[i] - hz) * inv;
+    n[i] = (q + kRound) - kRound;
+    settled = settled && fabsf(q - n[i]) <= 0.5f - 0x1p-16f;  // false for NaN
   }
-  return codes;
+  if (!settled) {
+    settled = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = 0.5f * x[i] - hz, e = fmaf(-n[i], hs, d);  // exact
+      if (2.0f * fabsf(e) == hs) n[i] = (n[i] + copysignf(0.5f, e) + kRound) - kRound;
+      else settled = settled && fabsf(fmaf(d, inv, -n[i])) <= 0.5f - 0x1p-16f;
+    }
+    if (!settled) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v = w[i / 2];
+        const float xi = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(0.5f * xi - hz, hs)), 0.0f), 15.0f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];
+      }
+    }
+  }
+  // Four codes at a time as one whole number below 2^16, read off its bits.
+  const float a0 = fmaf(fmaf(fmaf(n[3], 16.0f, n[2]), 16.0f, n[1]), 16.0f, n[0]) + 8388608.0f;
+  const float a1 = fmaf(fmaf(fmaf(n[7], 16.0f, n[6]), 16.0f, n[5]), 16.0f, n[4]) + 8388608.0f;
+  return __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x5410);
 }
 
-// DH / 8 lanes per row: 16 bytes in, 4 bytes of codes out each.
+// DH / 8 lanes per row: 16 bytes in, 4 bytes of codes out each, kRowsAhead
+// rows (of K and V) in flight.
+constexpr int kRowsAhead = 2;
 template <int DH>
 __global__ void __launch_bounds__(kThreads) append_kernel(StoreArgs a) {
-  constexpr int LPR = DH / 8, ROWS = kThreads / LPR;
+  constexpr int LPR = DH / 8, ROWS = kThreads / LPR, U = kRowsAhead;
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % LPR;
-  const long long n = static_cast<long long>(a.B) * a.G * a.T;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * ROWS; r0 < n; r0 += static_cast<long long>(gridDim.x) * ROWS) {
-    const long long r = r0 + threadIdx.x / LPR;
-    const long long bg = r / a.T;
-    const long long at = r < n ? cache_row(a, bg, static_cast<int>(r - bg * a.T)) : -1;
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-    if (at >= 0) {
-      k = __ldg(reinterpret_cast<const uint4*>(a.K + r * DH) + l);
-      v = __ldg(reinterpret_cast<const uint4*>(a.V + r * DH) + l);
+  const uint32_t n = static_cast<uint32_t>(a.B) * a.G * a.T, step = gridDim.x * ROWS;
+  for (uint32_t r0 = blockIdx.x * ROWS; r0 < n; r0 += U * step) {
+    long long at[U];
+    uint4 k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t r = r0 + u * step + threadIdx.x / LPR;
+      at[u] = r0 + u * step < n && r < n ? cache_row(a, r) : -1;
+      k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at[u] >= 0) {
+        k[u] = __ldg(reinterpret_cast<const uint4*>(a.K + static_cast<size_t>(r) * DH) + l);
+        v[u] = __ldg(reinterpret_cast<const uint4*>(a.V + static_cast<size_t>(r) * DH) + l);
+      }
     }
-    uint32_t mk, mv;
-    const uint32_t ck = quantise<LPR>(k, &mk), cv = quantise<LPR>(v, &mv);
-    if (at < 0) continue;
-    reinterpret_cast<uint32_t*>(a.c.k_codes)[at * LPR + l] = ck;
-    reinterpret_cast<uint32_t*>(a.c.v_codes)[at * LPR + l] = cv;
-    if (l == 0) reinterpret_cast<uint2*>(a.c.meta)[at] = make_uint2(mk, mv);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t mk, mv;
+      const uint32_t ck = quantise<LPR>(k[u], &mk), cv = quantise<LPR>(v[u], &mv);
+      if (at[u] < 0) continue;
+      reinterpret_cast<uint32_t*>(a.c.k_codes)[at[u] * LPR + l] = ck;
+      reinterpret_cast<uint32_t*>(a.c.v_codes)[at[u] * LPR + l] = cv;
+      if (l == 0) reinterpret_cast<uint2*>(a.c.meta)[at[u]] = make_uint2(mk, mv);
+    }
   }
 }
 
 __device__ __forceinline__ uint4 decode8(uint32_t codes, uint32_t meta) {
-  const float s = bf16_f(meta & 0xffffu), z = bf16_f(meta >> 16);
+  const float s = bf16_f(meta & 0xffffu), z = __uint_as_float(meta & 0xffff0000u);
   float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, static_cast<float>((codes >> (4 * i)) & 15u), z);
+  for (int i = 0; i < 8; ++i)  // a code in the low bits of 2^23 is 2^23 + code
+    x[i] = fmaf(s, __uint_as_float(((codes >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, z);
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
-  constexpr int LPR = DH / 8, ROWS = kThreads / LPR;
+  constexpr int LPR = DH / 8, ROWS = kThreads / LPR, U = kRowsAhead;
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % LPR;
-  const long long n = static_cast<long long>(a.B) * a.G * a.T;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * ROWS; r0 < n; r0 += static_cast<long long>(gridDim.x) * ROWS) {
-    const long long r = r0 + threadIdx.x / LPR;
-    if (r >= n) break;
-    const long long bg = r / a.T;
-    const long long at = cache_row(a, bg, static_cast<int>(r - bg * a.T));
-    if (at < 0) continue;
-    const uint2 m = reinterpret_cast<const uint2*>(a.c.meta)[at];
-    reinterpret_cast<uint4*>(a.Ko + r * DH)[l] = decode8(reinterpret_cast<const uint32_t*>(a.c.k_codes)[at * LPR + l], m.x);
-    reinterpret_cast<uint4*>(a.Vo + r * DH)[l] = decode8(reinterpret_cast<const uint32_t*>(a.c.v_codes)[at * LPR + l], m.y);
+  const uint32_t n = static_cast<uint32_t>(a.B) * a.G * a.T, step = gridDim.x * ROWS;
+  for (uint32_t r0 = blockIdx.x * ROWS; r0 < n; r0 += U * step) {
+    uint32_t k[U], v[U];
+    uint2 m[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t r = r0 + u * step + threadIdx.x / LPR;
+      const long long at = r0 + u * step < n && r < n ? cache_row(a, r) : -1;
+      on[u] = at >= 0;
+      if (!on[u]) continue;
+      m[u] = reinterpret_cast<const uint2*>(a.c.meta)[at];
+      k[u] = reinterpret_cast<const uint32_t*>(a.c.k_codes)[at * LPR + l];
+      v[u] = reinterpret_cast<const uint32_t*>(a.c.v_codes)[at * LPR + l];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!on[u]) continue;
+      const size_t r = r0 + u * step + threadIdx.x / LPR;
+      reinterpret_cast<uint4*>(a.Ko + r * DH)[l] = decode8(k[u], m[u].x);
+      reinterpret_cast<uint4*>(a.Vo + r * DH)[l] = decode8(v[u], m[u].y);
+    }
   }
 }
 
