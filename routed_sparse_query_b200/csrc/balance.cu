@@ -63,28 +63,31 @@ __device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool 
   }
 }
 
-// z to probabilities; the log of the sum of exp. exp and log are the fast
-// ones (2^-21 of the result near 1, 2^-19 for e^-20): far inside what fp32
-// sums over the rows keep.
+// z to exp(z - max); 1 / their sum and log sum exp(z). exp and log are the
+// hardware's (2^-21); z and the maximum are scaled to base 2 in one multiply-
+// add, so that the rounding of the scaled maximum is common to all and leaves
+// the probabilities.
 template <int LANES, int PER>
-__device__ __forceinline__ float softmax(float (&z)[PER]) {
+__device__ __forceinline__ void softmax(float (&z)[PER], float* inv, float* lse) {
+  constexpr float kLog2e = 1.44269504088896340736f;
   float m = z[0];
 #pragma unroll
   for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float c = -m * kLog2e;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    z[i] = __expf(z[i] - m);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z[i]) : "f"(fmaf(z[i], kLog2e, c)));
     s += z[i];
   }
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float inv = __fdividef(1.0f, s);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) z[i] *= inv;
-  return m + __logf(s);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(*inv) : "f"(s));
+  float l2;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l2) : "f"(s));
+  *lse = fmaf(l2, 0.69314718055994530942f, m);
 }
 
 // Threads of a CTA: `rows` rows x G groups x LANES lanes (the rest idle),
@@ -108,9 +111,9 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
     psum[i] = 0.0f;
     cnt[i] = 0;
   }
-  auto count = [&](int j, bool live) {
+  auto count = [&](int j) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) cnt[i] += live && j == q + i * LANES ? 1 : 0;
+    for (int i = 0; i < PER; ++i) cnt[i] += j == q + i * LANES ? 1 : 0;
   };
   const long long zs = step * a.G * a.M, is = step * a.G * a.k;
   long long r = static_cast<long long>(blockIdx.x) * rows + rl;
@@ -137,15 +140,16 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const float lse = softmax<LANES, PER>(z[u]);
+      float inv, lse;
+      softmax<LANES, PER>(z[u], &inv, &lse);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) psum[i] += live[u] ? z[u][i] : 0.0f;
+      for (int i = 0; i < PER; ++i) psum[i] = live[u] ? fmaf(z[u][i], inv, psum[i]) : psum[i];
       if (a.k <= 2) {
-        count(sel[u][0], live[u]);
-        count(sel[u][1], live[u]);
+        count(live[u] ? sel[u][0] : -1);
+        count(live[u] ? sel[u][1] : -1);
       } else if (live[u]) {
         const int32_t* ip = ip0 + u * is;
-        for (int s = 0; s < a.k; ++s) count(__ldg(ip + s), true);
+        for (int s = 0; s < a.k; ++s) count(__ldg(ip + s));
       }
       if (live[u] && q == 0) lsum = fmaf(lse, lse, lsum);
       if (live[u] && q == 0 && g == 0) ++n;
@@ -279,10 +283,13 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) grad_kernel(GradAr
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const float lse = softmax<LANES, PER>(z[u]);
-      float mean = 0.0f;
+      float inv, lse, mean = 0.0f;
+      softmax<LANES, PER>(z[u], &inv, &lse);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) mean = fmaf(z[u][i], f[i], mean);
+      for (int i = 0; i < PER; ++i) {
+        z[u][i] *= inv;
+        mean = fmaf(z[u][i], f[i], mean);
+      }
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
 #pragma unroll

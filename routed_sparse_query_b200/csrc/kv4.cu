@@ -27,6 +27,49 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float bf16_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ __nv_bfloat162 bf162(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
 
+// Two fp32 values worked on by one instruction.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 make_f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float f2_lo(F2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f2_hi(F2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// n / d for n < 2^31 by a multiplication (a 32-bit division costs about 20
+// instructions, two of them per row).
+struct Divisor {
+  uint32_t mul;
+  int shift;
+  explicit Divisor(uint32_t d) : shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  Divisor() : mul(0), shift(0) {}
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct StoreArgs {
   const uint16_t* K;   // [B][G][T][dh]
   const uint16_t* V;
@@ -37,13 +80,14 @@ struct StoreArgs {
   int start0;          // without start
   const int32_t* count;
   int B, G, T;
+  Divisor by_T, by_G;
 };
 
 // Cache row of row r = (b G + g) T + t (fewer than 2^31), or -1: t is past the
 // sequence's count, or the position is outside the cache (recorded, unless it
 // is before position 0).
 __device__ __forceinline__ long long cache_row(const StoreArgs& a, uint32_t r) {
-  const uint32_t bg = r / static_cast<uint32_t>(a.T), b = bg / static_cast<uint32_t>(a.G);
+  const uint32_t bg = a.by_T.of(r), b = a.by_G.of(bg);
   const int t = static_cast<int>(r - bg * a.T);
   if (a.count != nullptr && t >= a.count[b]) return -1;
   const long long p = static_cast<long long>(a.start != nullptr ? a.start[b] : a.start0) + t;
@@ -55,29 +99,41 @@ __device__ __forceinline__ long long cache_row(const StoreArgs& a, uint32_t r) {
   return static_cast<long long>(bg) * a.c.capacity + p;
 }
 
-// This lane's 8 codes of a row, and the row's (scale, zero) word.
-//
-// The quotient (x - zero) / scale is needed to the nearest whole number only:
-// a product with the approximate reciprocal is within 2^-17 of it, so that
-// quotients further than 2^-16 from a half are settled. Of the others nearly
-// all are halves exactly (values and scales have 8 bits), which an exact
-// remainder shows; what is left (and scales whose reciprocal leaves fp32)
-// takes the definition's division. Adding 1.5 * 2^23 rounds to a whole number,
-// half to even.
-template <int LPR>
-__device__ __forceinline__ uint32_t quantise(uint4 raw, uint32_t* meta) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  constexpr float kRound = 12582912.0f;
-  float x[8];
-  float zero_if_finite = 0.0f;
+// Eight codes by the definition's division.
+__device__ __noinline__ uint32_t divide_codes(uint4 p, float hz, float hs) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+  uint32_t codes = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    zero_if_finite = fmaf(x[i], 0.0f, zero_if_finite);
+    const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    codes |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(0.5f * x - hz, hs)), 0.0f), 15.0f)) << (4 * i);
   }
+  return codes;
+}
+
+// This lane's 16 elements of a row (two 16-byte pieces) to codes, 8 per word;
+// the row's (scale, zero) word.
+//
+// The quotient (x - zero) / scale is needed to the nearest whole number only.
+// A product with the approximate reciprocal is within 2^-17 of it; rounded to
+// a multiple of 2^-15 first (adding 384 does that) it is exact where the
+// quotient is a half, so that adding 1.5 * 2^23 then rounds halves to even as
+// the definition's division does. Halves are frequent (0.2 % of the elements:
+// values and scales have 8 bits), quotients within 2^-16 of one are not: they
+// show in the remainder and take the definition's division, as do scales
+// whose reciprocal leaves fp32.
+template <int LPR>
+__device__ __forceinline__ uint2 quantise(uint4 p0, uint4 p1, uint32_t* meta) {
+  const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+  constexpr float kRound = 12582912.0f, kGrid = 384.0f;
+  // Pairs are unpacked where they are used: registers are what limits the loads in flight.
+  auto pair = [&](int i) { return make_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)); };
+  F2 zero_if_finite = make_f2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) zero_if_finite = fma2(pair(i), make_f2(0.0f, 0.0f), zero_if_finite);
   __nv_bfloat162 lo2 = bf162(w[0]), hi2 = lo2;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
+  for (int i = 1; i < 8; ++i) {
     lo2 = __hmin2(lo2, bf162(w[i]));
     hi2 = __hmax2(hi2, bf162(w[i]));
   }
@@ -88,85 +144,93 @@ __device__ __forceinline__ uint32_t quantise(uint4 raw, uint32_t* meta) {
   }
   const float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
   const uint32_t group = ((1u << LPR) - 1u) << (threadIdx.x % 32 / LPR * LPR);
-  if ((__ballot_sync(0xffffffffu, zero_if_finite != 0.0f) & group) != 0u) {  // NaN != 0
+  const float bad = f2_lo(zero_if_finite) + f2_hi(zero_if_finite);
+  if ((__ballot_sync(0xffffffffu, bad != 0.0f) & group) != 0u) {  // NaN != 0
     *meta = 0x7fff7fffu;
-    return 0u;
+    return make_uint2(0u, 0u);
   }
   // Halved throughout: max - min of two bf16 may pass the largest fp32, and
-  // halving is exact.
-  const uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(0.5f * hi - 0.5f * lo, 7.5f)));
+  // halving is exact. The scale's quotient as a product, too, unless that ends
+  // within 4 units of a border between two bf16.
+  const float range = 0.5f * hi - 0.5f * lo;
+  float sq = range * (1.0f / 7.5f);
+  if ((__float_as_uint(sq) & 0xffffu) - 0x7ffcu <= 8u || !(sq > 1e-30f)) sq = __fdiv_rn(range, 7.5f);
+  const uint16_t sb = __bfloat16_as_ushort(__float2bfloat16_rn(sq));
   const float s = bf16_f(sb), hs = 0.5f * s, hz = 0.5f * lo;
   *meta = sb | (__float_as_uint(lo) & 0xffff0000u);
-  if (!(s > 0.0f)) return 0u;
-  const float inv = __fdividef(1.0f, hs);
-  bool settled = true;
-  float n[8];
+  if (!(s > 0.0f)) return make_uint2(0u, 0u);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(hs));
+  auto distance = [&](int i) { return fma2(pair(i), make_f2(0.5f, 0.5f), make_f2(-hz, -hz)); };  // (x - zero) / 2
+  auto quotient = [&](F2 d) { return add2(add2(mul2(d, make_f2(inv, inv)), make_f2(kGrid, kGrid)), make_f2(-kGrid, -kGrid)); };
+  auto whole = [&](F2 q) { return add2(add2(q, make_f2(kRound, kRound)), make_f2(-kRound, -kRound)); };
+  float off = 0.0f;  // the largest distance from a whole number
+  uint32_t half[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = (0.5f * x[i] - hz) * inv;
-    n[i] = (q + kRound) - kRound;
-    settled = settled && fabsf(q - n[i]) <= 0.5f - 0x1p-16f;  // false for NaN
+  for (int j = 0; j < 4; ++j) {
+    F2 n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const F2 q = quotient(distance(2 * j + i));
+      n[i] = whole(q);
+      const F2 f = fma2(n[i], make_f2(-1.0f, -1.0f), q);
+      off = max_nan(off, fabsf(f2_lo(f)), fabsf(f2_hi(f)));
+    }
+    // Four codes as one whole number below 2^16, read off its bits: (n0 + 256 n2) + 16 (n1 + 256 n3).
+    const F2 t = fma2(n[1], make_f2(256.0f, 256.0f), n[0]);
+    half[j] = __float_as_uint(fmaf(f2_hi(t), 16.0f, f2_lo(t)) + 8388608.0f);
   }
-  if (!settled) {
-    settled = true;
+  if (!(off < 0.5f)) {
+    // A half whose remainder is not zero (or a NaN): the division.
+    bool settled = off == 0.5f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float d = 0.5f * x[i] - hz, e = fmaf(-n[i], hs, d);  // exact
-      if (2.0f * fabsf(e) == hs) n[i] = (n[i] + copysignf(0.5f, e) + kRound) - kRound;
-      else settled = settled && fabsf(fmaf(d, inv, -n[i])) <= 0.5f - 0x1p-16f;
+      const F2 d = distance(i), q = quotient(d), f = fma2(whole(q), make_f2(-1.0f, -1.0f), q), e = fma2(q, make_f2(-hs, -hs), d);
+      settled = settled && (fabsf(f2_lo(f)) != 0.5f || f2_lo(e) == 0.0f) && (fabsf(f2_hi(f)) != 0.5f || f2_hi(e) == 0.0f);
     }
-    if (!settled) {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t v = w[i / 2];
-        const float xi = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16);
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(0.5f * xi - hz, hs)), 0.0f), 15.0f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) n[j] = i == j ? c : n[j];
-      }
-    }
+    if (!settled) return make_uint2(divide_codes(p0, hz, hs), divide_codes(p1, hz, hs));
   }
-  // Four codes at a time as one whole number below 2^16, read off its bits.
-  const float a0 = fmaf(fmaf(fmaf(n[3], 16.0f, n[2]), 16.0f, n[1]), 16.0f, n[0]) + 8388608.0f;
-  const float a1 = fmaf(fmaf(fmaf(n[7], 16.0f, n[6]), 16.0f, n[5]), 16.0f, n[4]) + 8388608.0f;
-  return __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x5410);
+  return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
 }
 
-// DH / 8 lanes per row: 16 bytes in, 4 bytes of codes out each, kRowsAhead
-// rows (of K and V) in flight.
-constexpr int kRowsAhead = 2;
+// DH / 16 lanes per row, each with the 16-byte pieces l and l + lanes (what a
+// row needs once is shared by 16 elements; 8 lanes per row: 34 us against 27
+// at 4 x 8192 tokens).
 template <int DH>
-__global__ void __launch_bounds__(kThreads) append_kernel(StoreArgs a) {
-  constexpr int LPR = DH / 8, ROWS = kThreads / LPR, U = kRowsAhead;
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(StoreArgs a) {
+  constexpr int LPR = DH / 16, ROWS = kThreads / LPR;
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % LPR;
   const uint32_t n = static_cast<uint32_t>(a.B) * a.G * a.T, step = gridDim.x * ROWS;
-  for (uint32_t r0 = blockIdx.x * ROWS; r0 < n; r0 += U * step) {
-    long long at[U];
-    uint4 k[U], v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t r = r0 + u * step + threadIdx.x / LPR;
-      at[u] = r0 + u * step < n && r < n ? cache_row(a, r) : -1;
-      k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (at[u] >= 0) {
-        k[u] = __ldg(reinterpret_cast<const uint4*>(a.K + static_cast<size_t>(r) * DH) + l);
-        v[u] = __ldg(reinterpret_cast<const uint4*>(a.V + static_cast<size_t>(r) * DH) + l);
-      }
+  for (uint32_t r0 = blockIdx.x * ROWS; r0 < n; r0 += step) {
+    const uint32_t r = r0 + threadIdx.x / LPR;
+    const long long at = r < n ? cache_row(a, r) : -1;
+    uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
+    if (at >= 0) {
+      const uint4* kp = reinterpret_cast<const uint4*>(a.K + static_cast<size_t>(r) * DH) + l;
+      const uint4* vp = reinterpret_cast<const uint4*>(a.V + static_cast<size_t>(r) * DH) + l;
+      k0 = __ldg(kp);
+      k1 = __ldg(kp + LPR);
+      v0 = __ldg(vp);
+      v1 = __ldg(vp + LPR);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t mk, mv;
-      const uint32_t ck = quantise<LPR>(k[u], &mk), cv = quantise<LPR>(v[u], &mv);
-      if (at[u] < 0) continue;
-      reinterpret_cast<uint32_t*>(a.c.k_codes)[at[u] * LPR + l] = ck;
-      reinterpret_cast<uint32_t*>(a.c.v_codes)[at[u] * LPR + l] = cv;
-      if (l == 0) reinterpret_cast<uint2*>(a.c.meta)[at[u]] = make_uint2(mk, mv);
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {  // K, then V (loaded above): one copy of the code, half the registers
+      uint32_t m;
+      const uint2 c = quantise<LPR>(k0, k1, &m);
+      k0 = v0;
+      k1 = v1;
+      if (at < 0) continue;
+      uint32_t* d = reinterpret_cast<uint32_t*>(t == 0 ? a.c.k_codes : a.c.v_codes) + at * (DH / 8) + l;
+      d[0] = c.x;
+      d[LPR] = c.y;
+      if (l == 0) reinterpret_cast<uint32_t*>(a.c.meta)[2 * at + t] = m;
     }
   }
 }
 
+constexpr int kRowsAhead = 2;  // rows of a thread in flight
 __device__ __forceinline__ uint4 decode8(uint32_t codes, uint32_t meta) {
   const float s = bf16_f(meta & 0xffffu), z = __uint_as_float(meta & 0xffff0000u);
   float x[8];
@@ -880,8 +944,8 @@ AttnWs attn_ws(int B, int G, int H, int dh) {
   return w;
 }
 
-unsigned store_ctas(int B, int G, int T, int dh) {
-  const long long rows = kThreads / (dh / 8), n = (static_cast<long long>(B) * G * T + rows - 1) / rows;
+unsigned store_ctas(int B, int G, int T, int rows) {  // rows per CTA
+  const long long n = (static_cast<long long>(B) * G * T + rows - 1) / rows;
   return static_cast<unsigned>(n < 148 * 8 ? n : 148 * 8);
 }
 
@@ -890,16 +954,16 @@ using namespace kv4_impl;
 
 int kv4_append(int B, int G, int T, int dh, const uint16_t* K, const uint16_t* V, const int32_t* start, int start0,
                const int32_t* count, const gqe_kv4& cache, void* stream) {
-  const StoreArgs a{K, V, nullptr, nullptr, cache, start, start0, count, B, G, T};
-  const dim3 grid(store_ctas(B, G, T, dh));
+  const StoreArgs a{K, V, nullptr, nullptr, cache, start, start0, count, B, G, T, Divisor(T), Divisor(G)};
+  const dim3 grid(store_ctas(B, G, T, kv4_impl::kThreads / (dh / 16)));
   return dh == 64 ? launch_pdl(append_kernel<64>, grid, dim3(kv4_impl::kThreads), 0, stream, a)
                   : launch_pdl(append_kernel<32>, grid, dim3(kv4_impl::kThreads), 0, stream, a);
 }
 
 int kv4_read(int B, int G, int T, int dh, const gqe_kv4& cache, const int32_t* start, const int32_t* count,
              uint16_t* K, uint16_t* V, void* stream) {
-  const StoreArgs a{nullptr, nullptr, K, V, cache, start, 0, count, B, G, T};
-  const dim3 grid(store_ctas(B, G, T, dh));
+  const StoreArgs a{nullptr, nullptr, K, V, cache, start, 0, count, B, G, T, Divisor(T), Divisor(G)};
+  const dim3 grid(store_ctas(B, G, T, kv4_impl::kThreads / (dh / 8)));
   return dh == 64 ? launch_pdl(read_kernel<64>, grid, dim3(kv4_impl::kThreads), 0, stream, a)
                   : launch_pdl(read_kernel<32>, grid, dim3(kv4_impl::kThreads), 0, stream, a);
 }

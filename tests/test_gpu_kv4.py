@@ -112,6 +112,40 @@ def test_append_and_read(rsq, B, G, T, dh, cap):
     assert rsq.gqe_read_status() == 0
 
 
+@pytest.mark.parametrize("dh", [32, 64])
+def test_codes_are_the_definitions(rsq, dh):
+    # Bit for bit over many rows: quotients that are halves (codes half to
+    # even), next to a half, scales at a border between two bf16, and scales of
+    # every magnitude.
+    rng = np.random.default_rng(7)
+    n = 1 << 16
+    x = rng.standard_normal((n, dh))
+    x[n // 4: n // 2] = rng.integers(-64, 65, (n // 4, dh)) / 8.0  # few bits: many halves
+    x[n // 2: 3 * n // 4] *= np.exp2(rng.integers(-120, 120, (n // 4, 1)))
+    x[3 * n // 4:] = rng.standard_normal((n // 4, 1)) * 50 + rng.standard_normal((n // 4, dh))  # far from zero
+    # zero -7.5, scale 1: 7.5 + x for small x of both signs, down to what fp32 loses.
+    small = np.exp2(-rng.integers(0, 40, (64, dh)).astype(np.float64)) * rng.choice([-1, 1], (64, dh))
+    small[:, 0], small[:, 1] = -7.5, 7.5
+    # (max - min) / 15 half way between two bf16, and next to it.
+    border = rng.random((64, dh)) * 15
+    border[:, 0], border[:, 1] = 15.0, -0.05859375 * np.exp2(-(np.arange(64) % 4))
+    x = np.concatenate([x, small, border]).astype(np.float32)
+    x = op.bf16_round(x)
+    T = 64
+    B = x.shape[0] // T
+    K = torch.from_numpy(x).to(torch.bfloat16).view(B, 1, T, dh)
+    V = K.flip(2).contiguous()
+    t, cache = new_cache(rsq, B, 1, T, dh, fill=0)
+    rsq.gqe_kv4_append(rsq.GQEConfig(B, T, 64, 1, 1, 1, dh, 0), K.cuda(), V.cuda(), None, None, cache)
+    got = host(t)
+    for data, codes, at in ((K, got[0], 0), (V, got[1], 2)):
+        c, s, z = op.kv4_quantise(data.float().numpy())
+        meta = got[2].float().numpy()
+        assert np.array_equal(meta[..., at], s) and np.array_equal(meta[..., at + 1], z)
+        assert np.array_equal(op.kv4_unpack(codes.numpy()), c)
+    assert rsq.gqe_read_status() == 0
+
+
 def test_positions_outside_the_cache(rsq):
     B, G, T, dh, cap = 4, 2, 6, 64, 32
     K, V = rows(B, G, T, dh, 5), rows(B, G, T, dh, 6)
