@@ -453,7 +453,8 @@ gqe_status gqe_qk_rope(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf
  * not read and may be NULL. dQ, dQs, dK in the layout of Q, Qs, K, each may
  * be its dQo, dQso, dKo. dw_q, dw_k [d_head] (overwritten; summed over every
  * row in a fixed order), or NULL: not computed; with GQE_ROPE_NORM only.
- * ws >= gqe_workspace_bytes(cfg, GQE_WS_QK_ROPE) bytes.
+ * ws >= gqe_workspace_bytes(cfg, GQE_WS_QK_ROPE) bytes; calls sharing one ws
+ * must not overlap on the GPU.
  */
 gqe_status gqe_qk_rope_bwd(const gqe_config* cfg, const gqe_rope* rope, const gqe_bf16* Q, const gqe_bf16* Qs,
                            const gqe_bf16* K, const int32_t* slot_pos, const float* dQo, const float* dQso,
@@ -463,6 +464,8 @@ gqe_status gqe_qk_rope_bwd(const gqe_config* cfg, const gqe_rope* rope, const gq
 /*
  * The router's logits alone: z[row, e] = x[row] . W_r[:, e] + b_r[e], fp32
  * (one fp32 sum; the certified selection is gqe_router_topk's). z [B*T, N].
+ * GQE_ERR_UNSUPPORTED where W_r and 16 rows of x (4 d_model N + 32 d_model
+ * bytes) exceed 227 KB.
  */
 gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const float* W_r, const float* b_r, float* z,
                              gqe_stream_t stream);
@@ -487,7 +490,8 @@ gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const flo
  * z [B*T, N] fp32; idx [B*T, G, k] int32 (gqe_router_topk; an entry outside
  * 0..M-1 counts for no expert); mask [B*T] bytes, 0 = not counted (its logits
  * are not looked at, its dz is 0), or NULL. No row counted: loss and dz 0.
- * ws >= gqe_workspace_bytes(cfg, GQE_WS_BALANCE) bytes.
+ * ws >= gqe_workspace_bytes(cfg, GQE_WS_BALANCE) bytes; calls sharing one ws
+ * must not overlap on the GPU.
  */
 gqe_status gqe_balance_stats(const gqe_config* cfg, const float* z, const int32_t* idx, const uint8_t* mask,
                              int32_t* counts, float* sums, void* ws, size_t ws_bytes, gqe_stream_t stream);
@@ -587,7 +591,8 @@ gqe_status gqe_decode_step_rope(const gqe_config* cfg, const gqe_rope* rope, con
  * Decode step over the 4-bit cache, sequences of their own lengths: the new
  * token of sequence b is at position lens[b] (its cache holds 0..lens[b]-1),
  * is stored there and attends to lens[b] + 1 keys. lens[b] = -1: an idle
- * sequence of a padded batch (nothing stored, y[b] = 0). lens is not changed.
+ * sequence of a padded batch (nothing stored, y[b] = 0; its x has to be
+ * finite). lens is not changed.
  * A lens[b] of cfg->T or more is a caller's error: nothing is stored from
  * capacity on (recorded, GQE_ERR_DEVICE_CHECK), at most cfg->T keys are read.
  *   cfg->T   the most keys any sequence has after the step, <= capacity;

@@ -400,7 +400,9 @@ size_t gqe_workspace_bytes(const gqe_config* cfg, int which) {
     return decode_kv4_ws(*cfg).total;
   }
   if (which == GQE_WS_BACKWARD_AUX)
-    return check_cfg(cfg) != GQE_OK || (cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u ? 0 : bwd_aux_ws(*cfg).total;
+    return check_cfg(cfg) != GQE_OK || (cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u || router_logits_smem(*cfg) > kMaxSmem
+               ? 0
+               : bwd_aux_ws(*cfg).total;
   if (cfg != nullptr && (which == GQE_WS_DECODE || which == GQE_WS_DENSE_DECODE)) {
     // Decode: the per-token buffers have B rows; T is the cache length.
     gqe_config c1 = decode_rows_cfg(*cfg);
@@ -773,7 +775,7 @@ gqe_status gqe_layer_bwd_aux(const gqe_config* cfg, const gqe_rope* rope, const 
                              size_t ws_bytes, gqe_stream_t stream) {
   gqe_status s = check_cfg(cfg);
   if (s != GQE_OK) return s;
-  if ((cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u) return GQE_ERR_UNSUPPORTED;
+  if ((cfg->flags & ~GQE_FLAG_WS_CLEAN) != 0u || router_logits_smem(*cfg) > kMaxSmem) return GQE_ERR_UNSUPPORTED;
   if (rope != nullptr && (s = check_rope(*cfg, rope)) != GQE_OK) return s;
   if ((dw_qn != nullptr || dw_kn != nullptr) && (rope == nullptr || (rope->flags & GQE_ROPE_NORM) == 0u))
     return GQE_ERR_INVALID;
@@ -837,6 +839,7 @@ gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const flo
   const gqe_status s = check_cfg(cfg);
   if (s != GQE_OK) return s;
   if (!all_aligned(x) || !all_aligned(W_r, static_cast<const float*>(z)) || !aligned_to(b_r, 4)) return GQE_ERR_INVALID;
+  if (router_logits_smem(*cfg) > kMaxSmem) return GQE_ERR_UNSUPPORTED;
   return cuda_status(router_logits(*cfg, x, W_r, b_r, z, stream));
 }
 
@@ -973,7 +976,7 @@ const char* gqe_status_string(gqe_status s) {
   }
 }
 
-int gqe_version(void) { return 100; }
+int gqe_version(void) { return 101; }
 
 }  // extern "C"
 

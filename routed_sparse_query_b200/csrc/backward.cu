@@ -40,7 +40,6 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 // router forms them), 16 rows per CTA; W_r and the 16 rows of x are staged
 // in shared memory, then thread (row i, expert e) of a pass takes one dot
 // product over d.
-constexpr int kLogitRows = 16;
 __global__ void __launch_bounds__(256) logits_kernel(const uint16_t* x, const float* W_r, const float* b_r,
                                                      float* z, long long R, int d, int N) {
   extern __shared__ float4 Ws4[];  // W_r [d][N] (d N is a multiple of 4: d is one of 64), then x rows [16][d] bf16
@@ -370,7 +369,7 @@ int bwd_pack(const gqe_config& c, const float* dQr, const float* dQs, const floa
 int router_logits(const gqe_config& c, const uint16_t* x, const float* W_r, const float* b_r, float* z, void* stream) {
   const long long R = static_cast<long long>(c.B) * c.T;
   const int N = c.G * c.M;
-  const int smem = c.d_model * N * static_cast<int>(sizeof(float)) + kLogitRows * c.d_model * 2;
+  const int smem = static_cast<int>(router_logits_smem(c));
   cudaError_t e = static_cast<cudaError_t>(ensure_smem<logits_kernel>(smem));
   if (e != cudaSuccess) return e;
   logits_kernel<<<static_cast<unsigned>((R + kLogitRows - 1) / kLogitRows), 256, smem,

@@ -50,16 +50,16 @@ __device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool 
   if constexpr (EXACT && PER % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(zp + i));
+      const float4 v = *reinterpret_cast<const float4*>(zp + i);
       z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
     }
   } else if constexpr (EXACT && PER == 2) {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(zp));
+    const float2 v = *reinterpret_cast<const float2*>(zp);
     z[0] = v.x; z[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (q + i * LANES < M) z[i] = __ldg(zp + q + i * LANES);
+      if (q + i * LANES < M) z[i] = zp[q + i * LANES];
   }
 }
 
@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
       const int32_t* ip = ip0 + u * is;
       sel[u][0] = sel[u][1] = -1;
       if (at && a.k == 2) {
-        const int2 v = __ldg(reinterpret_cast<const int2*>(ip));
+        const int2 v = *reinterpret_cast<const int2*>(ip);
         sel[u][0] = v.x;
         sel[u][1] = v.y;
       } else if (at && a.k == 1) {
-        sel[u][0] = __ldg(ip);
+        sel[u][0] = *ip;
       }
     }
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
         count(live[u] ? sel[u][1] : -1);
       } else if (live[u]) {
         const int32_t* ip = ip0 + u * is;
-        for (int s = 0; s < a.k; ++s) count(__ldg(ip + s));
+        for (int s = 0; s < a.k; ++s) count(ip[s]);
       }
       if (live[u] && q == 0) lsum = fmaf(lse, lse, lsum);
       if (live[u] && q == 0 && g == 0) ++n;

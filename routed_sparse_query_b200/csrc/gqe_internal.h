@@ -195,7 +195,12 @@ int bwd_attention_tc(const gqe_config& c, const uint16_t* Qv, const uint16_t* Qs
                      const uint16_t* V, const uint16_t* dO16, const float* Drow, const float* lse, float* stats,
                      float* dQr, float* dQs, float* dKp, float* dVp, void* stream);
 int bwd_colsum(const float* dz, float* db, long long R, int N, void* stream);
-// Router logits z [R, N] in fp32 (backward.cu).
+// Router logits z [R, N] in fp32 (backward.cu); W_r and 16 rows of x are staged in shared memory.
+constexpr size_t kMaxSmem = 227 * 1024;
+constexpr int kLogitRows = 16;
+inline size_t router_logits_smem(const gqe_config& c) {
+  return static_cast<size_t>(c.d_model) * c.G * c.M * sizeof(float) + static_cast<size_t>(kLogitRows) * c.d_model * 2;
+}
 int router_logits(const gqe_config& c, const uint16_t* x, const float* W_r, const float* b_r, float* z, void* stream);
 
 // Query/key norm and rotation (rope.cu). Rows of one operand: element 0 of

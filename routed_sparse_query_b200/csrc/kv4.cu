@@ -210,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(StoreArgs a) {
     if (at >= 0) {
       const uint4* kp = reinterpret_cast<const uint4*>(a.K + static_cast<size_t>(r) * DH) + l;
       const uint4* vp = reinterpret_cast<const uint4*>(a.V + static_cast<size_t>(r) * DH) + l;
-      k0 = __ldg(kp);
-      k1 = __ldg(kp + LPR);
-      v0 = __ldg(vp);
-      v1 = __ldg(vp + LPR);
+      k0 = *kp;
+      k1 = *(kp + LPR);
+      v0 = *vp;
+      v1 = *(vp + LPR);
     }
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {  // K, then V (loaded above): one copy of the code, half the registers
@@ -286,12 +286,15 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    eight elements. q goes in as q 2^(14 - e), e the exponent of the head's
 //    largest element: exact but for elements 2^-38 of that. Then
 //    s = scale_k sum(q n) + zero_k sum(q) in fp32.
-//  - Output, dims x heads, over the keys: 0x4300 | n is the bf16 128 + n. The
-//    weight operand is p scale_v in bf16 (fp16 would not hold the range of the
-//    scales); 136 times the sum of the same rounded weights is taken off
-//    again, which leaves sum p scale_v (n - 8), and the rest, sum p (zero_v +
-//    8 scale_v), is kept in fp32. The rounding of p thus meets codes around
-//    zero, |n - 8| <= 8.
+//  - Output, dims x heads, over the keys: with n in the upper four mantissa
+//    bits, 0x4180 | n << 3 is the bf16 16 + n. The weight operand is p scale_v
+//    in bf16 (fp16 would not hold the range of the scales); 24 times the sum of
+//    the same rounded weights is taken off again, which leaves sum p scale_v
+//    (n - 8), and the rest, sum p (zero_v + 8 scale_v), is kept in fp32. The
+//    rounding of p thus meets codes around zero, |n - 8| <= 8. The tensor cores
+//    cut their sums off where they would round, always downwards: each tile's
+//    sums start from zero and join the running ones in fp32 (carried on in the
+//    accumulator, and with 128 + n, the 64 x 32k outputs were 1.3 % off).
 //  - Up to 4 heads per group: the heads sit in the even columns, 4 / HP times
 //    over (HP = 1, 2 or 4 >= the group's heads), so the scores' accumulator
 //    holds one head per lane and every copy of the column can take other keys:
@@ -360,6 +363,13 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -367,11 +377,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// (x & 0x000f000f) | one in one instruction: with both masks as constants the
+// (x & 0x00780078) | one in one instruction: with both masks as constants the
 // compiler emits two, so `one` comes from a register that it cannot see into.
 __device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t one) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(x), "r"(one));
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xEA;" : "=r"(r) : "r"(x), "r"(one));
   return r;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -438,9 +448,9 @@ struct Warp {
   static constexpr int SUB = kTile / 16;
   uint32_t qf[NB][KS][2];               // B fragments of the queries (column lr)
   float fac[NB][HPL], qsum[NB][HPL];    // of this lane's score columns
-  float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][4];
+  float m[NB][HPL], l[NB][HPL], zs[NB][HPL], acc[NB][MT][2 * HPL];  // acc: rows lr, then lr + 8
   int lr, lc;
-  uint32_t k128;  // 0x43004300, bf16 128 twice
+  uint32_t k16;  // 0x41804180, bf16 16 twice
 
   __device__ __forceinline__ void start(const AttnArgs& a, int b, int g, int hp) {
     const int H = heads_of_group(a, g);
@@ -451,7 +461,7 @@ struct Warp {
       float v[DH / 4], mx = 0.0f, sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < DH / 4; i += 8) {
-        const uint4 w = h < H ? __ldg(reinterpret_cast<const uint4*>(query_row(a, b, g, h, DH) + lc * (DH / 4) + i))
+        const uint4 w = h < H ? *reinterpret_cast<const uint4*>(query_row(a, b, g, h, DH) + lc * (DH / 4) + i)
                               : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -492,10 +502,9 @@ struct Warp {
         l[nb][j] = zs[nb][j] = 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[nb][t][i] = 0.0f;
-      }
+        for (int i = 0; i < 2 * HPL; ++i) acc[nb][t][i] = 0.0f;
     }
   }
 
@@ -588,7 +597,7 @@ struct Warp {
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             acc[nb][t][j] *= f;
-            acc[nb][t][j + 2] *= f;
+            acc[nb][t][j + HPL] *= f;
           }
         }
     }
@@ -612,10 +621,11 @@ struct Warp {
           const uint32_t w = pack_bf16x2(w2[0], w2[1]);
           pk[nb][i][r] = w;
 #pragma unroll
-          for (int j = 0; j < HPL; ++j)  // the weights as rounded, of the codes' 128 + 8
-            zs[nb][j] = fmaf(-136.0f, __uint_as_float(j == 0 ? w << 16 : w & 0xffff0000u), zs[nb][j]);
+          for (int j = 0; j < HPL; ++j)  // the weights as rounded, of the codes' 16 + 8
+            zs[nb][j] = fmaf(-24.0f, __uint_as_float(j == 0 ? w << 16 : w & 0xffff0000u), zs[nb][j]);
         }
       }
+    float sum[NB][MT][4];  // of this tile
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       uint32_t pw[NB][2];
@@ -628,18 +638,30 @@ struct Warp {
       uint32_t x[2 * (DH / 32)];  // [32 elements][keys + 8 r]
       load_transposed(x, tva + 16 * u * S::ROW);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int hw = t / 2, sh = 8 * (t & 1);
+      for (int t = 0; t < MT; ++t) {  // nibbles 2 (t % 2), 2 (t % 2) + 1
         uint32_t f[4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          f[2 * r] = code_pair(x[2 * hw + r] >> sh, k128);
-          f[2 * r + 1] = code_pair(x[2 * hw + r] >> (sh + 4), k128);
+          const uint32_t v = x[2 * (t / 2) + r];
+          f[2 * r] = code_pair(t & 1 ? v >> 5 : v << 3, k16);
+          f[2 * r + 1] = code_pair(t & 1 ? v >> 9 : v >> 1, k16);
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_bf16(acc[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
+        for (int nb = 0; nb < NB; ++nb) {
+          if (u == 0) mma_bf16_first(sum[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
+          else mma_bf16(sum[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
+        }
       }
     }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < HPL; ++j) {
+          acc[nb][t][j] += sum[nb][t][j];
+          acc[nb][t][j + HPL] += sum[nb][t][j + 2];
+        }
   }
 
   // The unit's outputs (whole), or this warp's part of them into `slot`.
@@ -659,7 +681,7 @@ struct Warp {
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             acc[nb][t][j] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j], o);
-            acc[nb][t][j + 2] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j + 2], o);
+            acc[nb][t][j + HPL] += __shfl_xor_sync(0xffffffffu, acc[nb][t][j + HPL], o);
           }
         }
 #pragma unroll
@@ -673,7 +695,7 @@ struct Warp {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           o[2 * t] = (acc[nb][t][j] + z) * f;
-          o[2 * t + 1] = (acc[nb][t][j + 2] + z) * f;
+          o[2 * t + 1] = (acc[nb][t][j + HPL] + z) * f;
         }
         if (whole) {
           uint16_t* d = out_row(a, b, g, h, DH) + 4 * lr;
@@ -814,7 +836,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   Warp<DH, HPL, NB> w;
   w.lr = lane >> 2;
   w.lc = lane & 3;
-  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(w.k128));
+  asm volatile("mov.b32 %0, 0x41804180;" : "=r"(w.k16));
   // Columns per head set (HPL = 1): 1, 2 or 4 >= the group's heads.
   auto columns = [&](int g) {
     const int H = heads_of_group(a, g);

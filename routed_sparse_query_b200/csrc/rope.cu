@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a) {
     Coef c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float wa = w != nullptr ? __ldg(w + ln.elem_a(j)) : 1.0f, wb = w != nullptr ? __ldg(w + ln.elem_b(j)) : 1.0f;
+      const float wa = w != nullptr ? w[ln.elem_a(j)] : 1.0f, wb = w != nullptr ? w[ln.elem_b(j)] : 1.0f;
       c.ca[j] = cs[j] * wa;
       c.sb[j] = sn[j] * wb;
       c.sa[j] = sn[j] * wa;
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, kRopeBwdPerSm) rope_bwd_kernel(RopeA
   Weights w;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    w.wa[j] = wp != nullptr ? __ldg(wp + ln.elem_a(j)) : 1.0f;
-    w.wb[j] = wp != nullptr ? __ldg(wp + ln.elem_b(j)) : 1.0f;
+    w.wa[j] = wp != nullptr ? wp[ln.elem_a(j)] : 1.0f;
+    w.wb[j] = wp != nullptr ? wp[ln.elem_b(j)] : 1.0f;
     w.dwa[j] = w.dwb[j] = 0.0f;
   }
 #pragma unroll 1

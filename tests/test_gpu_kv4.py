@@ -243,6 +243,24 @@ def test_attention(rsq, name):
     assert rsq.gqe_read_status() == 0
 
 
+@pytest.mark.parametrize("T", [5000, 200000])
+def test_even_weights_over_many_keys(rsq, T):
+    # Hardly any score differs: the output is a mean of T values, sqrt(T)
+    # smaller than they are, and shows what the sums lose. Two roundings to bf16
+    # (the weights', the output's), each uniform within half a step and of
+    # 2^-8/sqrt(3) of the value at most as a standard deviation, in the values'
+    # own sizes: below 2^-8 together.
+    B, G, k, dh = 1, 2, 1, 64
+    t, cache = new_cache(rsq, B, G, (T + 15) // 16 * 16, dh, seed=3)
+    t[2][..., 3] = (-7.5 * t[2][..., 2].float()).to(torch.bfloat16)
+    q = (0.01 * torch.randn(B, G, k, dh, generator=torch.Generator().manual_seed(1))).to(torch.bfloat16)
+    cfg = rsq.GQEConfig(B, T, 64, G, 1, k, dh, 0)
+    got = run_attention(rsq, cfg, q, None, cache, None)
+    want, _ = attention_reference(q, None, host(t), [T], T, k)
+    err = got.double().numpy() - want
+    assert np.linalg.norm(err) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
 def test_large_and_small_values(rsq):
     # Queries and rows far from 1: nothing may leave fp32's range on the way.
     B, G, k, dh, T = 2, 2, 1, 64, 330
