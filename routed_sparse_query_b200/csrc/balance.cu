@@ -15,7 +15,7 @@
 // reads and writes 4 per logit). LANES lanes take one (row, group) pair, each
 // with PER of its logits in registers; a thread keeps to one group, so that
 // its partial sums stay in registers until the end. Sums run in fp32 per
-// thread and CTA and in fp64 over the CTAs, always in the same order.
+// thread and CTA and in fp64 over those, always in the same order.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -203,13 +203,19 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const float* part, int
   pdl_launch_dependents();
   const int cols = 2 * N + 2, col = blockIdx.x * 8 + threadIdx.x % 8;
   const bool whole = col < N || col == 2 * N + 1;
+  // A thread's few dozen parts in 32 bits, the threads' sums in 64 (a
+  // conversion per part had cost more than the rest of the kernel).
   double s = 0.0;
-  if (col < cols) {
+  if (col < cols && whole) {
+    int c = 0;
 #pragma unroll 8
-    for (int i = threadIdx.x / 8; i < ctas; i += kThreads / 8) {
-      const float v = part[static_cast<size_t>(i) * cols + col];
-      s += whole ? static_cast<double>(__float_as_int(v)) : static_cast<double>(v);
-    }
+    for (int i = threadIdx.x / 8; i < ctas; i += kThreads / 8) c += __float_as_int(part[static_cast<size_t>(i) * cols + col]);
+    s = c;
+  } else if (col < cols) {
+    float f = 0.0f;
+#pragma unroll 8
+    for (int i = threadIdx.x / 8; i < ctas; i += kThreads / 8) f += part[static_cast<size_t>(i) * cols + col];
+    s = f;
   }
   s += __shfl_xor_sync(0xffffffffu, s, 8);
   s += __shfl_xor_sync(0xffffffffu, s, 16);
