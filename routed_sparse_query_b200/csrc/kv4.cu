@@ -9,6 +9,9 @@
 // Every step of that is one IEEE fp32 operation, so the codes are the same
 // wherever it is computed. A row with an infinity or NaN gets scale = zero =
 // NaN: all of it reads as NaN.
+//
+// Storing 4 x 8192 tokens of 8 groups (86 MB): 27 us, bound by the arithmetic
+// (ALU 54 % busy); reading them back: 15 us (5.6 TB/s).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -301,17 +304,23 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    lane column lc forms the weights of head lc % HP for the 16-key blocks
 //    u = lc / HP (mod 4 / HP) only, and leaves 0 in the others. The copies'
 //    sums are added at the end of a unit. Without that one head's softmax
-//    costs what four heads' does (measured at 64 x 32k, one head in 7 of 8
-//    groups: see kv4_attn_kernel).
+//    costs what four heads' does (64 x 32k, one head in 7 of 8 groups: 149
+//    instructions per 16 keys against 164).
 //  - A transposed 8 x 8 move turns the weights from (key, head) to the second
 //    product's (head, keys) order.
 // The work is cut over warps: the tiles of 64 keys of all (sequence, group)
 // units, laid end to end, are dealt in equal contiguous shares, so that ragged
 // lengths, few long sequences and many short ones all fill the SMs alike. A
-// warp streams its tiles (cp.async: a bulk copy per array and tile cost more
-// instructions than its nine 512-byte pieces) through a ring of its own, across the units' borders, with its own running maximum and no CTA-wide barrier in the
-// loop. A unit that lies in one warp's share is written out by it; the parts
-// of the others are joined by a second kernel.
+// warp streams its tiles through a ring of its own, across the units' borders,
+// with its own running maximum and no CTA-wide barrier in the loop (by
+// cp.async: a bulk copy per array and tile took more instructions than its
+// nine 512-byte pieces). A unit that lies in one warp's share is written out
+// by it; the parts of the others are joined by a second kernel.
+//
+// Measured: 64 x 32768 keys, 8 groups, one or two heads each: 227 us (1.21 GB,
+// 82 % of the copy rate, the SMs at 1.62 GHz under the power cap; 203 us in a
+// short run); 192 x 32768: 97 % of the copy rate; ALU pipe 60 % and tensor pipe
+// 30 % busy. 1 x 2048 keys: 10 us, two launches.
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 64;   // keys per tile
@@ -876,54 +885,53 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   }
 }
 
-// Joins the parts of the units that lie in several shares: one CTA per unit,
-// H DH threads per part, as many parts at a time as the CTA has room for.
-constexpr int kJoinThreads = 512;
+// Joins the parts of the units that lie in several shares: one CTA per unit
+// and head, DH threads per part, blockDim / DH parts at a time (about as many
+// as a unit has: 1 x 1M keys have 297 per unit).
+constexpr int kJoinRows = 16;
 template <int DH>
-__global__ void __launch_bounds__(1024) kv4_join_kernel(AttnArgs a) {
-  extern __shared__ float jm[];  // [rows][H DH + 2 H]
+__global__ void __launch_bounds__(kJoinRows * DH) kv4_join_kernel(AttnArgs a) {
+  __shared__ float jo[kJoinRows * DH], jm[kJoinRows], jl[kJoinRows];
   pdl_wait();
   pdl_launch_dependents();
-  const int g = blockIdx.x % a.G, b = blockIdx.x / a.G;
+  const int u = blockIdx.x / a.H, h = blockIdx.x - u * a.H;
+  const int b = u / a.G, g = u - b * a.G;
   const int tb = tiles_of(keys_of(a, b));
-  if (tb == 0) return;
+  if (tb == 0 || h >= heads_of_group(a, g)) return;
   const long long share = a.starts[a.B], s0 = a.starts[b] + static_cast<long long>(g) * tb;
   const long long p0 = s0 / share, p1 = (s0 + tb - 1) / share;  // the warps of its tiles
   if (p0 == p1) return;
-  const int HD = a.H * DH, row = threadIdx.x / HD, rows = blockDim.x / HD, i = threadIdx.x % HD, h = i / DH;
-  const long long slot0 = p0 + blockIdx.x;
+  const int row = threadIdx.x / DH, rows = blockDim.x / DH, d = threadIdx.x % DH;
   const int parts = static_cast<int>(p1 - p0 + 1);
-  const bool on = h < heads_of_group(a, g);
-  float m = -INFINITY;
-  if (on)
+  const float2* ml = a.part_ml + (p0 + u) * a.H + h;
+  const float* po = a.part_o + ((p0 + u) * a.H + h) * DH + d;
+  float m = -INFINITY, o = 0.0f, l = 0.0f;
 #pragma unroll 4
-    for (int c = row; c < parts; c += rows) m = fmaxf(m, a.part_ml[(slot0 + c) * a.H + h].x);
+  for (int c = row; c < parts; c += rows) m = fmaxf(m, ml[static_cast<long long>(c) * a.H].x);
   const float mu = m == -INFINITY ? 0.0f : m;
-  float o = 0.0f, l = 0.0f;
-  if (on)
 #pragma unroll 4
-    for (int c = row; c < parts; c += rows) {
-      const float2 ml = a.part_ml[(slot0 + c) * a.H + h];
-      const float w = exp2_ftz(ml.x - mu);
-      l = fmaf(w, ml.y, l);
-      o = fmaf(w, a.part_o[(slot0 + c) * HD + i], o);
-    }
-  float* mine = jm + row * 3 * HD;
-  mine[i] = o;
-  mine[HD + i] = l;
-  mine[2 * HD + i] = m;
+  for (int c = row; c < parts; c += rows) {
+    const float2 v = ml[static_cast<long long>(c) * a.H];
+    const float w = exp2_ftz(v.x - mu);
+    l = fmaf(w, v.y, l);
+    o = fmaf(w, po[static_cast<long long>(c) * a.H * DH], o);
+  }
+  jo[threadIdx.x] = o;
+  if (d == 0) {
+    jm[row] = m;
+    jl[row] = l;
+  }
   __syncthreads();
-  if (row != 0 || !on) return;
-  float mx = m;
-  for (int r = 1; r < rows; ++r) mx = fmaxf(mx, jm[(r * 3 + 2) * HD + i]);
-  const float mxu = mx == -INFINITY ? 0.0f : mx;
+  if (row != 0) return;
+  for (int r = 1; r < rows; ++r) m = fmaxf(m, jm[r]);
+  const float all = m == -INFINITY ? 0.0f : m;
   o = l = 0.0f;
   for (int r = 0; r < rows; ++r) {
-    const float w = exp2_ftz(jm[(r * 3 + 2) * HD + i] - mxu);
-    l = fmaf(w, jm[(r * 3 + 1) * HD + i], l);
-    o = fmaf(w, jm[r * 3 * HD + i], o);
+    const float w = exp2_ftz(jm[r] - all);
+    l = fmaf(w, jl[r], l);
+    o = fmaf(w, jo[r * DH + d], o);
   }
-  out_row(a, b, g, h, DH)[i % DH] = __bfloat16_as_ushort(__float2bfloat16_rn(o / l));
+  out_row(a, b, g, h, DH)[d] = __bfloat16_as_ushort(__float2bfloat16_rn(o / l));
 }
 
 int attn_ctas(int B, int G, int T) {
@@ -948,9 +956,12 @@ int attention(const AttnArgs& a, void* stream) {
                 : a.H <= 8 ? launch_attn<DH, 2, 1>(a, stream)
                            : launch_attn<DH, 2, 2>(a, stream);
   if (e != cudaSuccess || a.T <= kTile) return e;  // one tile per unit: nothing to join
-  const int HD = a.H * DH, rows = HD >= kJoinThreads ? 1 : kJoinThreads / HD;
-  return launch_pdl(kv4_join_kernel<DH>, dim3(static_cast<unsigned>(a.B) * a.G), dim3(rows * HD),
-                    static_cast<size_t>(rows) * 3 * HD * 4, stream, a);
+  // Rows: as many as a unit has parts, but one wave of threads (33 x 5003 keys
+  // of 32 heads: 37 us with 16 rows, 29 with 4).
+  const long long units = static_cast<long long>(a.B) * a.G, parts = kMaxAttnWarps / units + 2;
+  int rows = 1;
+  while (rows < kJoinRows && rows < parts && units * a.H * DH * rows * 2 <= 148 * 2048) rows *= 2;
+  return launch_pdl(kv4_join_kernel<DH>, dim3(static_cast<unsigned>(units) * a.H), dim3(rows * DH), 0, stream, a);
 }
 
 // Workspace: the parts' slots, then the sequences' starts.

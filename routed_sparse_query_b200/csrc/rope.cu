@@ -16,8 +16,13 @@
 // neighbouring tokens: a warp reads whole 64-byte segments of a head. Bytes in
 // flight come from four rows per thread in the forward, from many threads in
 // the backward (64 registers; two or more rows per thread cost occupancy and
-// were no faster, nor were rows ahead through shared memory). The norm's weights are multiplied
-// into cos and sin once per token.
+// were no faster, nor were rows ahead through shared memory). The norm's
+// weights are multiplied into cos and sin once per token.
+//
+// Measured, 8 groups of d_head 64, share of the copy rate: forward of 4 x 8192
+// tokens 29 us (142 MB, 76 %), of 262144 tokens 202 us (1.14 GB, 87 %; 181 us
+// in a short run with one axis); backward of 4 x 8192 tokens and 25 heads
+// 91 us (524 MB, 89 %). 64 tokens: 7 us, the launch.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
