@@ -326,22 +326,23 @@ def gqa_dense_decode_step(cfg, x, W_q, W_k, W_v, W_o_dense, K_cache, V_cache, y,
 
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_byref = ctypes.byref
 
 
-def _call(name, dev, stream, *args):
-    """The C entry point on device `dev` and on `stream` (default: that device's
-    current stream)."""
+def _call(fn, dev, stream, *args):
+    """The C entry point `fn` on device `dev` and on `stream` (default: that
+    device's current stream)."""
     if dev == _current_device():
-        status = getattr(_lib, name)(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            status = getattr(_lib, name)(*args, _stream(stream))
-    if status != GQE_OK:
-        raise GQEError(status, name)
+            status = fn(*args, _stream(stream))
+    if status:
+        raise GQEError(status, fn.__name__)
 
 
 def _config(cfg) -> GQEConfig:
-    return cfg if isinstance(cfg, GQEConfig) else GQEConfig.of(cfg)
+    return cfg if type(cfg) is GQEConfig else GQEConfig.of(cfg)
 
 
 def _ws(ws, dev):
@@ -354,13 +355,13 @@ def _rope(rope, c, rows, dev):
     """`rope` (or None) checked against a call of `rows` tokens on `dev`."""
     if rope is None:
         return None
-    if rope._dev not in (-1, dev):
+    if rope._dev != dev and rope._dev != -1:
         raise ValueError(f"rope: on cuda:{rope._dev}, the call's other tensors on cuda:{dev}")
-    if rope._n_pos not in (None, rope.axes * rows):
+    if rope._n_pos is not None and rope._n_pos != rope.axes * rows:
         raise ValueError(f"rope.pos: {rope._n_pos} elements, {rope.axes * rows} are needed")
-    if rope._n_w - {c.d_head}:
+    if rope._n_w and rope._n_w != {c.d_head}:
         raise ValueError(f"rope.w_q, rope.w_k: {c.d_head} elements are needed")
-    return ctypes.byref(rope)
+    return _byref(rope)
 
 
 def _kv4(cache, c, dev):
@@ -368,50 +369,51 @@ def _kv4(cache, c, dev):
         raise ValueError(f"cache: on cuda:{cache._dev}, the call's other tensors on cuda:{dev}")
     if cache._shape != (c.B, c.G, c.d_head):
         raise ValueError(f"cache: made for (B, G, d_head) = {cache._shape}, not {(c.B, c.G, c.d_head)}")
-    return ctypes.byref(cache)
+    return _byref(cache)
 
 
 def gqe_qk_rope(cfg, rope, Q, Qs, K, slot_pos, Qo, Qso, Ko, stream=None):
     c = _config(cfg)
-    dev, R, dh = _first_device(Q, Qs, K), c.B * c.T, c.d_head
-    nq, nk = R * c.G * c.k * dh, R * c.G * dh
-    _call("gqe_qk_rope", dev, stream, ctypes.byref(c), _rope(rope, c, R, dev), _arg(Q, _BF16, nq, dev, "Q"),
-          _arg(Qs, _BF16, R * dh, dev, "Qs"), _arg(K, _BF16, nk, dev, "K"),
-          _arg(slot_pos, _I32, R * c.G * c.k, dev, "slot_pos"), _arg(Qo, _BF16, nq, dev, "Qo"),
-          _arg(Qso, _BF16, R * dh, dev, "Qso"), _arg(Ko, _BF16, nk, dev, "Ko"))
+    R, G, dh = c.B * c.T, c.G, c.d_head
+    dev, nq, ns, nk = _first_device(Q, Qs, K), R * G * c.k * dh, R * dh, R * G * dh
+    _call(_lib.gqe_qk_rope, dev, stream, _byref(c), _rope(rope, c, R, dev), _arg(Q, _BF16, nq, dev, "Q"),
+          _arg(Qs, _BF16, ns, dev, "Qs"), _arg(K, _BF16, nk, dev, "K"),
+          None if slot_pos is None else _arg(slot_pos, _I32, R * G * c.k, dev, "slot_pos"),
+          _arg(Qo, _BF16, nq, dev, "Qo"), _arg(Qso, _BF16, ns, dev, "Qso"), _arg(Ko, _BF16, nk, dev, "Ko"))
 
 
 def gqe_qk_rope_bwd(cfg, rope, Q, Qs, K, slot_pos, dQo, dQso, dKo, dQ, dQs, dK, dw_q, dw_k, ws, stream=None):
     c = _config(cfg)
-    dev, R, dh = _first_device(dQo, dQso, dKo), c.B * c.T, c.d_head
-    nq, ns, nk = R * c.G * c.k * dh, R * dh, R * c.G * dh
-    _call("gqe_qk_rope_bwd", dev, stream, ctypes.byref(c), _rope(rope, c, R, dev), _arg(Q, _BF16, nq, dev, "Q"),
+    R, G, dh = c.B * c.T, c.G, c.d_head
+    dev, nq, ns, nk = _first_device(dQo, dQso, dKo), R * G * c.k * dh, R * dh, R * G * dh
+    _call(_lib.gqe_qk_rope_bwd, dev, stream, _byref(c), _rope(rope, c, R, dev), _arg(Q, _BF16, nq, dev, "Q"),
           _arg(Qs, _BF16, ns, dev, "Qs"), _arg(K, _BF16, nk, dev, "K"),
-          _arg(slot_pos, _I32, R * c.G * c.k, dev, "slot_pos"), _arg(dQo, _F32, nq, dev, "dQo"),
-          _arg(dQso, _F32, ns, dev, "dQso"), _arg(dKo, _F32, nk, dev, "dKo"), _arg(dQ, _F32, nq, dev, "dQ"),
-          _arg(dQs, _F32, ns, dev, "dQs"), _arg(dK, _F32, nk, dev, "dK"), _arg(dw_q, _F32, dh, dev, "dw_q"),
-          _arg(dw_k, _F32, dh, dev, "dw_k"), *_ws(ws, dev))
+          None if slot_pos is None else _arg(slot_pos, _I32, R * G * c.k, dev, "slot_pos"),
+          _arg(dQo, _F32, nq, dev, "dQo"), _arg(dQso, _F32, ns, dev, "dQso"), _arg(dKo, _F32, nk, dev, "dKo"),
+          _arg(dQ, _F32, nq, dev, "dQ"), _arg(dQs, _F32, ns, dev, "dQs"), _arg(dK, _F32, nk, dev, "dK"),
+          _arg(dw_q, _F32, dh, dev, "dw_q"), _arg(dw_k, _F32, dh, dev, "dw_k"), *_ws(ws, dev))
 
 
 def gqe_router_logits(cfg, x, W_r, b_r, z, stream=None):
     c = _config(cfg)
     dev, R, N = _first_device(x), c.B * c.T, c.G * c.M
-    _call("gqe_router_logits", dev, stream, ctypes.byref(c), _arg(x, _BF16, R * c.d_model, dev, "x"),
+    _call(_lib.gqe_router_logits, dev, stream, _byref(c), _arg(x, _BF16, R * c.d_model, dev, "x"),
           _arg(W_r, _F32, c.d_model * N, dev, "W_r"), _arg(b_r, _F32, N, dev, "b_r"), _arg(z, _F32, R * N, dev, "z"))
 
 
 def gqe_balance_stats(cfg, z, idx, mask, counts, sums, ws, stream=None):
     c = _config(cfg)
-    dev, R, N = _first_device(z), c.B * c.T, c.G * c.M
-    _call("gqe_balance_stats", dev, stream, ctypes.byref(c), _arg(z, _F32, R * N, dev, "z"),
-          _arg(idx, _I32, R * c.G * c.k, dev, "idx"), _arg(mask, _U8, R, dev, "mask"),
+    dev, R, G = _first_device(z), c.B * c.T, c.G
+    N = G * c.M
+    _call(_lib.gqe_balance_stats, dev, stream, _byref(c), _arg(z, _F32, R * N, dev, "z"),
+          _arg(idx, _I32, R * G * c.k, dev, "idx"), _arg(mask, _U8, R, dev, "mask"),
           _arg(counts, _I32, N + 1, dev, "counts"), _arg(sums, _F32, N + 1, dev, "sums"), *_ws(ws, dev))
 
 
 def gqe_balance_loss(cfg, z, mask, counts, sums, c_balance, c_z, loss, dz, accumulate=False, stream=None):
     c = _config(cfg)
     dev, R, N = _first_device(counts), c.B * c.T, c.G * c.M
-    _call("gqe_balance_loss", dev, stream, ctypes.byref(c), _arg(z, _F32, R * N, dev, "z"),
+    _call(_lib.gqe_balance_loss, dev, stream, _byref(c), _arg(z, _F32, R * N, dev, "z"),
           _arg(mask, _U8, R, dev, "mask"), _arg(counts, _I32, N + 1, dev, "counts"),
           _arg(sums, _F32, N + 1, dev, "sums"), c_balance, c_z, _arg(loss, _F32, 3, dev, "loss"),
           _arg(dz, _F32, R * N, dev, "dz"), 1 if accumulate else 0)
@@ -419,26 +421,28 @@ def gqe_balance_loss(cfg, z, mask, counts, sums, c_balance, c_z, loss, dz, accum
 
 def gqe_kv4_append(cfg, K, V, start, count, cache, stream=None):
     c = _config(cfg)
-    dev, n = _first_device(K), c.B * c.G * c.T * c.d_head
-    _call("gqe_kv4_append", dev, stream, ctypes.byref(c), _arg(K, _BF16, n, dev, "K"), _arg(V, _BF16, n, dev, "V"),
-          _arg(start, _I32, c.B, dev, "start"), _arg(count, _I32, c.B, dev, "count"), _kv4(cache, c, dev))
+    B = c.B
+    dev, n = _first_device(K), B * c.G * c.T * c.d_head
+    _call(_lib.gqe_kv4_append, dev, stream, _byref(c), _arg(K, _BF16, n, dev, "K"), _arg(V, _BF16, n, dev, "V"),
+          _arg(start, _I32, B, dev, "start"), _arg(count, _I32, B, dev, "count"), _kv4(cache, c, dev))
 
 
 def gqe_kv4_read(cfg, cache, start, count, K, V, stream=None):
     c = _config(cfg)
-    dev, n = _first_device(K), c.B * c.G * c.T * c.d_head
-    _call("gqe_kv4_read", dev, stream, ctypes.byref(c), _kv4(cache, c, dev), _arg(start, _I32, c.B, dev, "start"),
-          _arg(count, _I32, c.B, dev, "count"), _arg(K, _BF16, n, dev, "K"), _arg(V, _BF16, n, dev, "V"))
+    B = c.B
+    dev, n = _first_device(K), B * c.G * c.T * c.d_head
+    _call(_lib.gqe_kv4_read, dev, stream, _byref(c), _kv4(cache, c, dev), _arg(start, _I32, B, dev, "start"),
+          _arg(count, _I32, B, dev, "count"), _arg(K, _BF16, n, dev, "K"), _arg(V, _BF16, n, dev, "V"))
 
 
 def gqe_kv4_attention(cfg, Q, Qs, cache, lens, out, ws, stream=None):
     """out [B, ldo]: ldo is its row length."""
     c = _config(cfg)
+    B, dh, ldo = c.B, c.d_head, out.shape[-1]
     dev = _first_device(Q)
-    ldo = out.shape[-1]
-    _call("gqe_kv4_attention", dev, stream, ctypes.byref(c), _arg(Q, _BF16, c.B * c.G * c.k * c.d_head, dev, "Q"),
-          _arg(Qs, _BF16, c.B * c.d_head, dev, "Qs"), _kv4(cache, c, dev), _arg(lens, _I32, c.B, dev, "lens"),
-          _arg(out, _BF16, c.B * ldo, dev, "out"), ldo, *_ws(ws, dev))
+    _call(_lib.gqe_kv4_attention, dev, stream, _byref(c), _arg(Q, _BF16, B * c.G * c.k * dh, dev, "Q"),
+          _arg(Qs, _BF16, B * dh, dev, "Qs"), _kv4(cache, c, dev), _arg(lens, _I32, B, dev, "lens"),
+          _arg(out, _BF16, B * ldo, dev, "out"), ldo, *_ws(ws, dev))
 
 
 def _layer_args(c, rows, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o):
@@ -454,7 +458,7 @@ def _layer_args(c, rows, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o):
 def gqe_layer_fwd_rope(cfg, rope, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, y, ws, stream=None):
     c = _config(cfg)
     dev, R = _first_device(x), c.B * c.T
-    _call("gqe_layer_fwd_rope", dev, stream, ctypes.byref(c), _rope(rope, c, R, dev),
+    _call(_lib.gqe_layer_fwd_rope, dev, stream, ctypes.byref(c), _rope(rope, c, R, dev),
           *_layer_args(c, R, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o), _arg(y, _BF16, R * c.d_model, dev, "y"),
           *_ws(ws, dev))
 
@@ -469,7 +473,7 @@ def gqe_layer_bwd_aux(cfg, rope, balance, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o,
     grads = [(dy, R * d, "dy"), (dx, R * d, "dx"), (dW_r, d * N, "dW_r"), (db_r, N, "db_r"), (dW_q, d * N * dh, "dW_q"),
              (dW_qs, d * dh, "dW_qs"), (dW_k, d * c.G * dh, "dW_k"), (dW_v, d * c.G * dh, "dW_v"),
              (dW_o, (c.k * c.G + 2) * dh * d, "dW_o"), (dw_qn, dh, "dw_qn"), (dw_kn, dh, "dw_kn")]
-    _call("gqe_layer_bwd_aux", dev, stream, ctypes.byref(c), _rope(rope, c, R, dev),
+    _call(_lib.gqe_layer_bwd_aux, dev, stream, ctypes.byref(c), _rope(rope, c, R, dev),
           None if balance is None else ctypes.byref(balance),
           *_layer_args(c, R, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o),
           *(_arg(t, _F32, n, dev, what) for t, n, what in grads), *_ws(ws, dev))
@@ -480,7 +484,7 @@ def gqe_decode_step_rope(cfg, rope, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, K_cac
     c = _config(cfg)
     dev, cap = _first_device(x), int(K_cache.shape[2])
     n = c.B * c.G * cap * c.d_head
-    _call("gqe_decode_step_rope", dev, stream, ctypes.byref(c), _rope(rope, c, c.B, dev),
+    _call(_lib.gqe_decode_step_rope, dev, stream, ctypes.byref(c), _rope(rope, c, c.B, dev),
           *_layer_args(c, c.B, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o), _arg(K_cache, _BF16, n, dev, "K_cache"),
           _arg(V_cache, _BF16, n, dev, "V_cache"), cap, _arg(y, _BF16, c.B * c.d_model, dev, "y"), *_ws(ws, dev))
 
@@ -488,7 +492,7 @@ def gqe_decode_step_rope(cfg, rope, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, K_cac
 def gqe_decode_step_kv4(cfg, rope, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o, cache, lens, y, ws, stream=None):
     c = _config(cfg)
     dev = _first_device(x)
-    _call("gqe_decode_step_kv4", dev, stream, ctypes.byref(c), _rope(rope, c, c.B, dev),
+    _call(_lib.gqe_decode_step_kv4, dev, stream, ctypes.byref(c), _rope(rope, c, c.B, dev),
           *_layer_args(c, c.B, dev, x, W_r, b_r, W_q, W_qs, W_k, W_v, W_o), _kv4(cache, c, dev),
           _arg(lens, _I32, c.B, dev, "lens"), _arg(y, _BF16, c.B * c.d_model, dev, "y"), *_ws(ws, dev))
 

@@ -454,8 +454,8 @@ using namespace rope_impl;
 
 // Heads one CTA walks: all of them where the token tiles alone fill the SMs
 // (the angles are then formed once per token), fewer for short batches.
-static int heads_per_cta(long long tiles, int H) {
-  long long chunks = (kRopeCtas + tiles - 1) / tiles;
+static int heads_per_cta(long long tiles, int H, int ctas = kRopeCtas) {
+  long long chunks = (ctas + tiles - 1) / tiles;
   chunks = chunks < 1 ? 1 : chunks > H ? H : chunks;
   return static_cast<int>((H + chunks - 1) / chunks);
 }
@@ -490,8 +490,10 @@ static int launch_bwd(const RopeArgs& a, const RopeBwdArgs& d, int ctas, float* 
 int rope_bwd(RopeArgs a, RopeBwdArgs d, int dh, float* dw_q, float* dw_k, void* ws, void* stream) {
   const int tok = rope_impl::kThreads / (dh / 8), Hq = a.n[0] + a.n[1], Hk = a.n[2];
   const long long tiles = (a.R + tok - 1) / tok;
-  // Runs of heads of about one length in both classes.
-  const int hpc = heads_per_cta(tiles, Hq + Hk);
+  // Runs of heads of about one length in both classes; few tiles: one run per
+  // resident CTA (2048 tokens of 17 heads: 10.3 us on the device against 11.3;
+  // 10000 tokens: 25.5 against 23.6).
+  const int hpc = heads_per_cta(tiles, Hq + Hk, 4 * tiles < kRopeBwdCtas ? kRopeBwdCtas : kRopeCtas);
   const int nq = (Hq + hpc - 1) / hpc, nk = (Hk + hpc - 1) / hpc;
   a.hpc = nq > 0 ? (Hq + nq - 1) / nq : 1;
   d.hpc_k = nk > 0 ? (Hk + nk - 1) / nk : 1;

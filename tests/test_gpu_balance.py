@@ -28,6 +28,7 @@ def rsq():
 CASES = {
     "one_row": (1, 1, 2, 2, 1, 0.0, None),
     "layer_2k": (1, 2048, 8, 2, 1, 0.0, None),
+    "layer_2049": (1, 2049, 8, 2, 1, 0.0, None),  # one row more than one cluster takes
     "pool_masked": (2, 777, 8, 4, 2, 2.0, 0.7),
     "m1": (1, 33, 4, 1, 1, 0.0, None),
     "m3_g5": (3, 41, 5, 3, 2, 0.5, 0.5),
