@@ -239,7 +239,7 @@ struct RopeBwdArgs {
   float* part;  // [CTAs][d_head] partial weight gradients (set by the launcher)
   int cq, hpc_k;  // CTAs of the queries, heads per item of the keys (set by the launcher)
 };
-constexpr int kRopeCtas = 148 * 8;  // CTAs of 256 threads that fill the SMs
+constexpr int kRopeCtas = 148 * 4;  // resident CTAs of the forward
 constexpr int kRopeBwdPerSm = 4;
 constexpr int kRopeBwdCtas = 148 * kRopeBwdPerSm;
 int rope_fwd(RopeArgs a, int dh, void* stream);

@@ -394,6 +394,44 @@ def pos_at(pos, x, at):
     return torch.cat([u * th.cos() - v * th.sin(), u * th.sin() + v * th.cos()], -1)
 
 
+def test_captured_training_step(rsq):
+    # Forward with positions and backward with both extras, captured on another
+    # stream (the layer's side stream joins the capture) and replayed on new
+    # inputs, with a workspace declared clean.
+    s = SHAPES["b2_t70"]
+    d = device_inputs(synth.make_layer_inputs(s, seed=8))
+    pos = Positions(rsq, s, s.R, axes=3, far=500)
+    cfg = rsq.GQEConfig.of(s, rsq.GQE_FLAG_WS_CLEAN)
+    R, N, dh, dm = s.R, s.N, s.d_head, s.d_model
+    f = lambda *shape: torch.zeros(shape, device="cuda")  # noqa: E731
+    grads = [f(R, dm), f(dm, N), f(N), f(dm, N * dh), f(dm, dh), f(dm, s.G * dh), f(dm, s.G * dh),
+             f((s.k * s.G + 2) * dh, dm), f(dh), f(dh)]
+    counts, sums, loss = torch.zeros(N + 1, dtype=torch.int32, device="cuda"), f(N + 1), f(3)
+    balance = rsq.GQEBalance.of(counts, sums, loss, None, 0.1, 0.01)
+    dy, y = torch.randn(R, dm, generator=torch.Generator().manual_seed(5)).cuda(), torch.empty(R, dm, dtype=torch.bfloat16, device="cuda")
+    wf, wb = (torch.zeros(rsq.gqe_workspace_bytes(cfg, k), dtype=torch.uint8, device="cuda")
+              for k in (rsq.GQE_WS_LAYER, rsq.GQE_WS_BACKWARD_AUX))
+
+    def step():
+        rsq.gqe_layer_fwd_rope(cfg, pos.rope, d["x"], *weights(d), y, wf)
+        rsq.gqe_layer_bwd_aux(cfg, pos.rope, balance, d["x"], *weights(d), dy, *grads, wb)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    d["x"].copy_(d["x"].flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, loss, counts, *grads)]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, loss, counts, *grads)))
+    assert int(counts[-1]) == R and int(counts[:-1].sum()) == R * s.G * s.k
+    assert rsq.gqe_read_status() == 0
+
+
 def test_lengths_default_to_the_bound(rsq):
     s = LayerShape(B=2, T=33, d_model=64, G=2, M=2, k=1, d_head=64)
     d = device_inputs(synth.make_layer_inputs(s, seed=8))

@@ -38,7 +38,10 @@ CASES = {
     "norm_only": (1, 19, 2, 1, 64, 0, True, True, False, 1, 0, 1.0),
     "rotation_only": (1, 50, 2, 2, 64, 64, False, False, False, 1, 200000, 1.0),
     "scaled_axes4": (1, 129, 1, 1, 32, 32, True, True, False, 4, 3000, 1.25),
+    "axes4_default_positions": (3, 40, 2, 1, 32, 32, True, True, True, 4, 0, 1.0),
+    "dh32_usual": (2, 300, 3, 2, 32, 32, True, True, False, 2, 64, 1.0),
     "long": (1, 2500, 8, 1, 64, 64, True, True, False, 1, 0, 1.0),
+    "tiles_of_many_heads": (5, 1200, 8, 2, 64, 64, True, True, False, 1, 0, 1.0),
 }
 
 
