@@ -346,9 +346,7 @@ def _config(cfg) -> GQEConfig:
 
 
 def _ws(ws, dev):
-    if ws.get_device() != dev:
-        raise ValueError(f"ws: on cuda:{ws.get_device()}, the call's other tensors on cuda:{dev}")
-    return _ptr(ws), ws.numel() * ws.element_size()
+    return _arg(ws, ws.dtype, None, dev, "ws"), ws.nbytes
 
 
 def _rope(rope, c, rows, dev):

@@ -17,9 +17,11 @@
 // its partial sums stay in registers until the end. Sums run in fp32 per
 // thread and CTA and in fp64 over those, always in the same order.
 //
-// Measured: 262144 rows of 8 x 4 logits, k = 2, masked: 32 us (84 MB; 18 stats,
-// 3 finish, 10 gradient, whose logits come from L2): instructions and load
-// latency of short passes, not bandwidth. 2048 rows of 8 x 2: 13 us, two launches.
+// Measured: 262144 rows of 8 x 4 logits, k = 2, masked: 27 us (84 MB; in a
+// short run 13 for the two launches of stats, 9 for the gradient, whose logits
+// come from L2): load latency of short passes, not bandwidth. As many CTAs as
+// are resident, five rows per thread in flight: 23 us in the short run, 29 with
+// a quarter more CTAs and four rows. 2048 rows of 8 x 2: 12 us, two launches.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -33,8 +35,8 @@ namespace gqe {
 namespace balance_impl {
 
 constexpr int kThreads = 256;
-constexpr int kMaxCtas = 148 * 5;
-constexpr int kAhead = 4;  // rows of a thread in flight
+constexpr int kMaxCtas = 148 * 4;  // resident CTAs
+constexpr int kAhead = 5;  // rows of a thread in flight
 constexpr unsigned kCluster = 8;
 
 struct BalanceArgs {
@@ -110,7 +112,7 @@ __device__ __forceinline__ void softmax(float (&z)[PER], float* inv, float* lse)
 // first CTA adds up the others' sums out of their shared memory (no second
 // launch; see balance_stats).
 template <int LANES, int PER, bool EXACT, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(BalanceArgs a) {
   __shared__ float sp[kThreads * PER];
   __shared__ int sc[kThreads * PER];
   __shared__ float sl[kThreads];
@@ -139,20 +141,36 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
   for (long long r0 = r - rl; r0 < a.R; r0 += kAhead * step, r += kAhead * step, zp += kAhead * zs, ip0 += kAhead * is) {
     float z[kAhead][PER];
     bool live[kAhead];
-    int sel[kAhead][2];  // the first two selections (k <= 2 is the usual case)
+    int sel[kAhead][2];  // the selections of a row that counts, if k <= 2
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const bool at = in && r + u * step < a.R;
-      load_logits<LANES, PER, EXACT>(zp + u * zs, q, a.M, at, z[u]);
-      live[u] = at && (a.mask == nullptr || a.mask[r + u * step] != 0);
-      const int32_t* ip = ip0 + u * is;
+      live[u] = in && r + u * step < a.R;
+      load_logits<LANES, PER, EXACT>(zp + u * zs, q, a.M, live[u], z[u]);
       sel[u][0] = sel[u][1] = -1;
-      if (at && a.k == 2) {
-        const int2 v = *reinterpret_cast<const int2*>(ip);
-        sel[u][0] = v.x;
-        sel[u][1] = v.y;
-      } else if (at && a.k == 1) {
-        sel[u][0] = *ip;
+    }
+    // What is the same for all rows is asked once for the four of them.
+    if (a.k == 2) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (live[u]) {
+          const int2 v = *reinterpret_cast<const int2*>(ip0 + u * is);
+          sel[u][0] = v.x;
+          sel[u][1] = v.y;
+        }
+    } else if (a.k == 1) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (live[u]) sel[u][0] = ip0[u * is];
+    }
+    if (a.mask != nullptr) {
+      uint8_t on[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) on[u] = live[u] ? a.mask[r + u * step] : 0;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        live[u] = on[u] != 0;
+        sel[u][0] = live[u] ? sel[u][0] : -1;
+        sel[u][1] = live[u] ? sel[u][1] : -1;
       }
     }
 #pragma unroll
@@ -161,15 +179,21 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
       softmax<LANES, PER>(z[u], &inv, &lse);
 #pragma unroll
       for (int i = 0; i < PER; ++i) psum[i] = live[u] ? fmaf(z[u][i], inv, psum[i]) : psum[i];
-      if (a.k <= 2) {
-        count(live[u] ? sel[u][0] : -1);
-        count(live[u] ? sel[u][1] : -1);
-      } else if (live[u]) {
-        const int32_t* ip = ip0 + u * is;
-        for (int s = 0; s < a.k; ++s) count(ip[s]);
+      lsum = live[u] && q == 0 ? fmaf(lse, lse, lsum) : lsum;
+      n += live[u] ? 1 : 0;
+    }
+    if (a.k <= 2) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) count(sel[u][0]);
+      if (a.k == 2) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) count(sel[u][1]);
       }
-      if (live[u] && q == 0) lsum = fmaf(lse, lse, lsum);
-      if (live[u] && q == 0 && g == 0) ++n;
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (live[u])
+          for (int s = 0; s < a.k; ++s) count(ip0[u * is + s]);
     }
   }
 #pragma unroll
@@ -178,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) stats_kernel(Balan
     sc[tid * PER + i] = cnt[i];
   }
   sl[tid] = lsum;
-  sn[tid] = n;
+  sn[tid] = g == 0 && q == 0 ? n : 0;
   __syncthreads();
   const int N = a.G * a.M;
   __shared__ float fin[CLUSTER ? 2 * kMaxExperts + 2 : 1];
@@ -272,7 +296,7 @@ struct GradArgs {
 };
 
 template <int LANES, int PER, bool EXACT>
-__global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) grad_kernel(GradArgs a) {
+__global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int N = a.G * a.M, tid = threadIdx.x;
@@ -313,9 +337,12 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 5 : 3) grad_kernel(GradAr
     bool at[kAhead], live[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      at[u] = in && r + u * step < a.R;
+      at[u] = live[u] = in && r + u * step < a.R;
       load_logits<LANES, PER, EXACT>(a.z + at0 + u * zs, q, a.M, at[u], z[u]);
-      live[u] = at[u] && (a.mask == nullptr || a.mask[r + u * step] != 0);
+    }
+    if (a.mask != nullptr) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) live[u] = at[u] && a.mask[r + u * step] != 0;
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {

@@ -28,7 +28,8 @@ def rsq():
 CASES = {
     "one_row": (1, 1, 2, 2, 1, 0.0, None),
     "layer_2k": (1, 2048, 8, 2, 1, 0.0, None),
-    "layer_2049": (1, 2049, 8, 2, 1, 0.0, None),  # one row more than one cluster takes
+    "cluster_2560": (1, 2560, 8, 2, 1, 0.0, None),  # as many rows as one cluster takes, and one more
+    "cluster_2561": (1, 2561, 8, 2, 1, 0.0, None),
     "pool_masked": (2, 777, 8, 4, 2, 2.0, 0.7),
     "m1": (1, 33, 4, 1, 1, 0.0, None),
     "m3_g5": (3, 41, 5, 3, 2, 0.5, 0.5),
