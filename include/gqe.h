@@ -474,7 +474,7 @@ gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const flo
  * Balance loss of the router, in two steps. The pages say that a
  * load-balancing loss is used and give no formula; this is the usual product
  * of load and mean probability, per group. With p the softmax of a group's M
- * logits, n the counted rows, c[e] the counted rows that selected expert e:
+ * logits, n the counted rows, c[e] the entries of idx in them that name expert e:
  *   L_balance = (M/G) sum_e (c[e] / (k n)) * (1/n) sum_rows p[row, e]
  *   L_z       = 1/(n G) sum_{rows, g} (log sum_j exp z[row, g, j])^2
  *   loss      = c_balance * L_balance + c_z * L_z
@@ -490,6 +490,8 @@ gqe_status gqe_router_logits(const gqe_config* cfg, const gqe_bf16* x, const flo
  * z [B*T, N] fp32; idx [B*T, G, k] int32 (gqe_router_topk; an entry outside
  * 0..M-1 counts for no expert); mask [B*T] bytes, 0 = not counted (its logits
  * are not looked at, its dz is 0), or NULL. No row counted: loss and dz 0.
+ * A group's experts may be switched off by the lowest fp32 value or -inf; all
+ * of them by -inf has no probabilities (NaN).
  * ws >= gqe_workspace_bytes(cfg, GQE_WS_BALANCE) bytes; calls sharing one ws
  * must not overlap on the GPU.
  */
@@ -533,7 +535,8 @@ gqe_status gqe_kv4_read(const gqe_config* cfg, const gqe_kv4* cache, const int32
  * for the k routed heads of every group and, with Qs, the shared head (group
  * 0). lens [B] int32, clamped to 0..cfg->T (NULL: cfg->T <= capacity; cfg->T
  * sizes the launch, so a bound near the longest sequence is best). A sequence
- * without keys gets zeros.
+ * without keys gets zeros. Sums are fp32 and divided at the end: 32 keys |V|
+ * has to stay below 2^127.
  * Q [B, G, k, d_head] (dense heads: cfg->k = M); Qs [B, d_head] or NULL;
  * out [B, ldo], ldo a multiple of 8: head (g, s) at column (g*k + s)*d_head,
  * the shared head at k*G*d_head. At most 16 heads per group, B*G <= 65535.

@@ -257,8 +257,9 @@ __global__ void cast_kernel(const float* in, long long ldi, long long rows, int 
 // per-stream parts dKp, dVp [B, G k + 1, T, dh] of its k routed streams (and
 // of the shared head for group 0); each of dQ, dK, dV arrives in two parts
 // [2][...] that are added here (dKc non-null: dQ and dK are sums already, dK
-// in dKc [B, G, T, dh]). Each thread writes 8 adjacent columns; the segment bounds before dz are multiples of 32, so 8 columns never
-// straddle two of them.
+// in dKc [B, G, T, dh]). Each thread writes 8 adjacent columns; the segment
+// bounds before dz are multiples of 32, so 8 columns never straddle two of
+// them.
 __global__ void pack_grads_kernel(const float* dQr, const float* dQs, const float* dKp, const float* dVp,
                                   const float* dz, const int32_t* idx, const float* dKc, uint16_t* Y, long long R,
                                   int T, int G, int M, int k, int dh, int ld) {

@@ -36,7 +36,7 @@ namespace balance_impl {
 
 constexpr int kThreads = 256;
 constexpr int kMaxCtas = 148 * 4;  // resident CTAs
-constexpr int kAhead = 5;  // rows of a thread in flight
+constexpr int kAheadFew = 5, kAheadMany = 3;  // rows of a thread in flight, up to 4 logits each and more
 constexpr unsigned kCluster = 8;
 
 struct BalanceArgs {
@@ -81,9 +81,9 @@ __device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool 
 }
 
 // z to exp(z - max); 1 / their sum and log sum exp(z). exp and log are the
-// hardware's (2^-21); z and the maximum are scaled to base 2 in one multiply-
-// add, so that the rounding of the scaled maximum is common to all and leaves
-// the probabilities.
+// hardware's (2^-21). The maximum is taken off before the scaling to base 2,
+// which would overflow for a group of logits that are all the type's lowest
+// value (every expert switched off: equal probabilities).
 template <int LANES, int PER>
 __device__ __forceinline__ void softmax(float (&z)[PER], float* inv, float* lse) {
   constexpr float kLog2e = 1.44269504088896340736f;
@@ -92,11 +92,10 @@ __device__ __forceinline__ void softmax(float (&z)[PER], float* inv, float* lse)
   for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float c = -m * kLog2e;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z[i]) : "f"(fmaf(z[i], kLog2e, c)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z[i]) : "f"((z[i] - m) * kLog2e));
     s += z[i];
   }
 #pragma unroll
@@ -108,11 +107,12 @@ __device__ __forceinline__ void softmax(float (&z)[PER], float* inv, float* lse)
 }
 
 // Threads of a CTA: `rows` rows x G groups x LANES lanes (the rest idle),
-// kAhead rows of each thread in flight. CLUSTER: the grid is one cluster, whose
+// several rows of each thread in flight. CLUSTER: the grid is one cluster, whose
 // first CTA adds up the others' sums out of their shared memory (no second
 // launch; see balance_stats).
 template <int LANES, int PER, bool EXACT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(BalanceArgs a) {
+  constexpr int kAhead = PER <= 4 ? kAheadFew : kAheadMany;
   __shared__ float sp[kThreads * PER];
   __shared__ int sc[kThreads * PER];
   __shared__ float sl[kThreads];
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
       load_logits<LANES, PER, EXACT>(zp + u * zs, q, a.M, live[u], z[u]);
       sel[u][0] = sel[u][1] = -1;
     }
-    // What is the same for all rows is asked once for the four of them.
+    // What is the same for all rows is asked once for all of them.
     if (a.k == 2) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
@@ -297,6 +297,7 @@ struct GradArgs {
 
 template <int LANES, int PER, bool EXACT>
 __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradArgs a) {
+  constexpr int kAhead = PER <= 4 ? kAheadFew : kAheadMany;
   pdl_wait();
   pdl_launch_dependents();
   const int N = a.G * a.M, tid = threadIdx.x;
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradAr
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (tid == 0) {
       const double bal = static_cast<double>(a.M) / a.G * s / (a.k * n) / n, zl = a.sums[N] / (a.G * n);
-      a.loss[0] = static_cast<float>(a.c_balance * bal + a.c_z * zl);
+      // A factor of 0 leaves its term out, an infinite one too.
+      a.loss[0] = static_cast<float>(a.c_balance * bal + (a.c_z != 0.0f ? a.c_z * zl : 0.0));
       a.loss[1] = static_cast<float>(bal);
       a.loss[2] = static_cast<float>(zl);
     }
@@ -424,9 +426,9 @@ int balance_stats(const float* z, const int32_t* idx, const uint8_t* mask, long 
                   int32_t* counts, float* sums, void* ws, void* stream) {
   const BalanceArgs a{z, idx, mask, R, G, M, k, static_cast<float*>(ws), counts, sums};
   const int ctas = ctas_for(R, G, M), rows = balance_impl::kThreads / (G * (M <= 8 ? 1 : 8));
-  // Few rows, at most two rounds of kAhead per thread: one cluster, no second
+  // Few rows, at most ten per thread: one cluster, no second
   // launch (2048 rows of 8 x 2 logits, both calls: 12.9 us against 14.3).
-  if (R <= static_cast<long long>(kCluster) * rows * 2 * kAhead)
+  if (R <= static_cast<long long>(kCluster) * rows * 10)
     return with_shape(M, [&](auto s) {
       using S = decltype(s);
       cudaLaunchAttribute attr[2];

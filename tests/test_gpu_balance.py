@@ -129,6 +129,28 @@ def test_low_logits_and_indices_outside(rsq):
     assert np.allclose(got["dz"], ref["dz"], rtol=2.0 ** -12, atol=2.0 ** -15 * np.abs(ref["dz"]).max())
 
 
+def test_group_switched_off_and_wide_logits(rsq):
+    # A group whose experts all hold the type's lowest value has equal
+    # probabilities; lse^2 then passes fp32, and a factor of 0 leaves it out.
+    # p: a softmax of z - max, exact here up to one rounding of the difference.
+    case = (1, 40, 3, 4, 2, 0.0, None)
+    z, idx, _ = make(case)
+    zg = z.reshape(40, 3, 4)
+    zg[3, 1] = zg[17, 2] = np.finfo(np.float32).min
+    zg[5, 0] = (2.0e38, -2.0e38, 1.0, 2.0e38)
+    idx[9, 1] = (2, 2)  # an expert named twice counts twice
+    ref = op.balance(z.astype(np.float64), idx, None, 3, 4, 0.1, 0.0)
+    got = call(rsq, case, z, idx, None, 0.1, 0.0)
+    assert np.array_equal(got["counts"][:-1].reshape(3, 4), ref["counts"])
+    assert (np.abs(got["sums"][:-1].reshape(3, 4) - ref["psum"]) <= 2.0 ** -16 * ref["psum"]).all()
+    assert np.isinf(got["sums"][-1]) and np.isinf(got["loss"][2])
+    assert abs(got["loss"][1] - ref["loss"][1]) <= 2.0 ** -15 * ref["loss"][1]
+    assert abs(got["loss"][0] - ref["loss"][0]) <= 2.0 ** -14 * ref["loss"][0]
+    f = ref["counts"] / 80 - 0.25
+    size = 0.1 * 4 / 120 * ref["p"] * (np.abs(f) + (ref["p"] * np.abs(f)).sum(-1, keepdims=True))
+    assert (np.abs(got["dz"].reshape(40, 3, 4) - ref["dz"].reshape(40, 3, 4)) <= 2.0 ** -15 * size).all()
+
+
 def test_accumulates_and_sums_of_two_ranks(rsq):
     # dz += with accumulate; two halves of a batch with added statistics give
     # the whole batch's gradient.
