@@ -57,8 +57,19 @@ __device__ __forceinline__ void store_sum(int col, int N, double s, int32_t* cou
   else counts[N] = static_cast<int32_t>(s);
 }
 
-// Logits of one (row, group) pair: lane q holds experts q, q + LANES, ...
-// EXACT: M = PER in one lane, read in one piece.
+// Which logits of a (row, group) pair lane q holds: experts q, q + LANES, ...
+// EXACT: in one lane, all (M = PER); in several, runs of four (M a multiple of
+// 4; 262144 rows of one group of 64 experts: 75 us, 81 with single ones).
+template <int LANES, int PER, bool EXACT>
+__device__ __forceinline__ int expert_of(int q, int i) {
+  return EXACT && LANES > 1 ? i / 4 * 4 * LANES + 4 * q + i % 4 : q + i * LANES;
+}
+// Its place among the pair's LANES PER values.
+template <int LANES, int PER, bool EXACT>
+__device__ __forceinline__ int place_of(int j) {
+  return EXACT && LANES > 1 ? j / 4 % LANES * PER + j / (4 * LANES) * 4 + j % 4 : j % LANES * PER + j / LANES;
+}
+
 template <int LANES, int PER, bool EXACT>
 __device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool at, float (&z)[PER]) {
 #pragma unroll
@@ -67,7 +78,9 @@ __device__ __forceinline__ void load_logits(const float* zp, int q, int M, bool 
   if constexpr (EXACT && PER % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(zp + i);
+      const int j = expert_of<LANES, PER, EXACT>(q, i);
+      if (LANES > 1 && j >= M) continue;
+      const float4 v = *reinterpret_cast<const float4*>(zp + j);
       z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
     }
   } else if constexpr (EXACT && PER == 2) {
@@ -114,13 +127,22 @@ template <int LANES, int PER, bool EXACT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(BalanceArgs a) {
   constexpr int kAhead = PER <= 4 ? kAheadFew : kAheadMany;
   __shared__ float sp[kThreads * PER];
-  __shared__ int sc[kThreads * PER];
+  // Counts per thread; or, with several lanes to a pair, per CTA: lane q takes
+  // the row's selections q, q + LANES, ... and adds to their experts' (whole
+  // numbers: in any order; every lane comparing all k selections with its
+  // experts: 67 us against 57 at 262144 rows of 2 x 32, k = 4).
+  constexpr bool HIST = LANES > 1;
+  __shared__ int sc[HIST ? kMaxExperts : kThreads * PER];
   __shared__ float sl[kThreads];
   __shared__ int sn[kThreads];
-  pdl_wait();
-  pdl_launch_dependents();
   const int gl = a.G * LANES, rows = kThreads / gl;
   const int tid = threadIdx.x, rl = tid / gl, g = (tid % gl) / LANES, q = tid % LANES;
+  if (HIST) {
+    if (tid < kMaxExperts) sc[tid] = 0;
+    __syncthreads();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
   const bool in = rl < rows;
   const long long step = static_cast<long long>(gridDim.x) * rows;
   float psum[PER], lsum = 0.0f;
@@ -131,8 +153,12 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
     cnt[i] = 0;
   }
   auto count = [&](int j) {
+    if (HIST) {
+      if (j >= 0 && j < a.M) atomicAdd(&sc[g * a.M + j], 1);
+      return;
+    }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) cnt[i] += j == q + i * LANES ? 1 : 0;
+    for (int i = 0; i < PER; ++i) cnt[i] += j == expert_of<LANES, PER, EXACT>(q, i) ? 1 : 0;
   };
   const long long zs = step * a.G * a.M, is = step * a.G * a.k;
   long long r = static_cast<long long>(blockIdx.x) * rows + rl;
@@ -141,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
   for (long long r0 = r - rl; r0 < a.R; r0 += kAhead * step, r += kAhead * step, zp += kAhead * zs, ip0 += kAhead * is) {
     float z[kAhead][PER];
     bool live[kAhead];
-    int sel[kAhead][2];  // the selections of a row that counts, if k <= 2
+    int sel[kAhead][2];  // the selections of a row that counts, if k <= 2 (HIST: this lane's first)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       live[u] = in && r + u * step < a.R;
@@ -149,7 +175,11 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
       sel[u][0] = sel[u][1] = -1;
     }
     // What is the same for all rows is asked once for all of them.
-    if (a.k == 2) {
+    if (HIST) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (live[u] && q < a.k) sel[u][0] = ip0[u * is + q];
+    } else if (a.k == 2) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (live[u]) {
@@ -182,7 +212,14 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
       lsum = live[u] && q == 0 ? fmaf(lse, lse, lsum) : lsum;
       n += live[u] ? 1 : 0;
     }
-    if (a.k <= 2) {
+    if (HIST) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        count(sel[u][0]);
+        if (live[u])
+          for (int s = q + LANES; s < a.k; s += LANES) count(ip0[u * is + s]);
+      }
+    } else if (a.k <= 2) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) count(sel[u][0]);
       if (a.k == 2) {
@@ -199,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     sp[tid * PER + i] = psum[i];
-    sc[tid * PER + i] = cnt[i];
+    if (!HIST) sc[tid * PER + i] = cnt[i];
   }
   sl[tid] = lsum;
   sn[tid] = g == 0 && q == 0 ? n : 0;
@@ -212,10 +249,11 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
     float s = 0.0f;
     int c = 0;
     for (int r = 0; r < rows; ++r) {
-      const int at = ((r * a.G + eg) * LANES + j % LANES) * PER + j / LANES;
+      const int at = (r * a.G + eg) * LANES * PER + place_of<LANES, PER, EXACT>(j);
       s += sp[at];
-      c += sc[at];
+      c += HIST ? 0 : sc[at];
     }
+    if (HIST) c = sc[e];
     out[e] = __int_as_float(c);
     out[N + e] = s;
   }
@@ -325,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradAr
   float f[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int j = q + i * LANES;
+    const int j = expert_of<LANES, PER, EXACT>(q, i);
     f[i] = in && j < a.M ? static_cast<float>((static_cast<double>(a.counts[g * a.M + j]) * a.M - a.k * n) / (a.M * a.k * n))
                          : 0.0f;
   }
@@ -364,7 +402,9 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradAr
       if constexpr (EXACT && PER % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
-          float4* o = reinterpret_cast<float4*>(out + i);
+          const int j = expert_of<LANES, PER, EXACT>(q, i);
+          if (LANES > 1 && j >= a.M) continue;
+          float4* o = reinterpret_cast<float4*>(out + j);
           float4 v = make_float4(z[u][i], z[u][i + 1], z[u][i + 2], z[u][i + 3]);
           if (a.accumulate) {
             const float4 w = *o;
@@ -392,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) grad_kernel(GradAr
 }
 
 // Instantiation for M: up to 8 logits in one lane (1, 2, 4 and 8 in one
-// piece), more on 8 lanes.
+// piece), more on 8 lanes (multiples of 4 above 16 in pieces of four).
 template <int L, int P, bool E>
 struct Shape {
   static constexpr int LANES = L, PER = P;
@@ -407,8 +447,8 @@ int with_shape(int M, F f) {
   if (M < 4) return f(Shape<1, 4, false>{});
   if (M < 8) return f(Shape<1, 8, false>{});
   if (M <= 16) return f(Shape<8, 2, false>{});
-  if (M <= 32) return f(Shape<8, 4, false>{});
-  return f(Shape<8, 8, false>{});
+  if (M <= 32) return M % 4 == 0 ? f(Shape<8, 4, true>{}) : f(Shape<8, 4, false>{});
+  return M % 4 == 0 ? f(Shape<8, 8, true>{}) : f(Shape<8, 8, false>{});
 }
 
 int ctas_for(long long R, int G, int M) {

@@ -37,6 +37,12 @@ CASES = {
     "m13": (1, 90, 4, 13, 3, 1.0, 0.9),
     "m32_g2": (1, 65, 2, 32, 4, 0.0, None),
     "m64": (2, 50, 1, 64, 5, 1.0, 0.3),
+    "m16_all_selected": (1, 77, 2, 16, 16, 1.0, 0.8),
+    "m19_k9": (1, 3001, 2, 19, 9, 1.0, 0.8),
+    "m20": (3, 301, 3, 20, 2, 1.0, None),
+    "m40": (1, 999, 1, 40, 12, 2.0, 0.5),
+    "m61": (1, 64, 1, 61, 1, 0.0, 0.9),
+    "m64_long": (1, 20011, 1, 64, 8, 2.0, 0.9),
     "g32_m2": (1, 300, 32, 2, 1, 0.0, None),
     "nothing_counted": (1, 40, 4, 2, 1, 0.0, 0.0),
     "long": (1, 70001, 8, 4, 2, 2.0, 0.8),
