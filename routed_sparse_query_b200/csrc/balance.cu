@@ -22,6 +22,7 @@
 // come from L2): load latency of short passes, not bandwidth. As many CTAs as
 // are resident, five rows per thread in flight: 23 us in the short run, 29 with
 // a quarter more CTAs and four rows. 2048 rows of 8 x 2: 12 us, two launches.
+// 262144 rows of one group of 64, k = 4: 61 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
