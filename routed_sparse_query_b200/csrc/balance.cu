@@ -154,12 +154,12 @@ __global__ void __launch_bounds__(kThreads, PER <= 4 ? 4 : 3) stats_kernel(Balan
     cnt[i] = 0;
   }
   auto count = [&](int j) {
-    if (HIST) {
+    if constexpr (HIST) {
       if (j >= 0 && j < a.M) atomicAdd(&sc[g * a.M + j], 1);
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) cnt[i] += j == expert_of<LANES, PER, EXACT>(q, i) ? 1 : 0;
+      for (int i = 0; i < PER; ++i) cnt[i] += j == expert_of<LANES, PER, EXACT>(q, i) ? 1 : 0;
+    }
   };
   const long long zs = step * a.G * a.M, is = step * a.G * a.k;
   long long r = static_cast<long long>(blockIdx.x) * rows + rl;

@@ -12,6 +12,7 @@
 //
 // Storing 4 x 8192 tokens of 8 groups (86 MB): 26 us, bound by the arithmetic
 // (ALU 54 % busy); reading them back: 15 us (5.8 TB/s).
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 // Measured: 64 x 32768 keys, 8 groups, one or two heads each: 227 us (1.21 GB,
 // 82 % of the copy rate, the SMs at 1.62 GHz under the power cap; 203 us in a
 // short run); 192 x 32768: 97 % of the copy rate; ALU pipe 60 % and tensor pipe
-// 30 % busy. 1 x 2048 keys: 10 us, two launches.
+// 30 % busy. 1 x 2048 keys: 7.5 us, one launch (kv4_attn_unit_kernel).
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 64;   // keys per tile
@@ -334,6 +335,7 @@ struct AttnArgs {
   gqe_kv4 c;
   const int32_t* lens;
   int len_add, B, G, T, k, H;
+  int ctas;  // of a cluster (unit kernel)
   // Part of warp w and unit u = b G + g: slot w + u (along the shares, w + u
   // grows with every part, and a unit's parts are consecutive).
   float* part_o;       // [slots][H][dh]
@@ -675,8 +677,21 @@ struct Warp {
         }
   }
 
-  // The unit's outputs (whole), or this warp's part of them into `slot`.
-  __device__ __forceinline__ void finish(const AttnArgs& a, int b, int g, int hp, bool whole, long long slot) {
+  __device__ __forceinline__ void any_tile(const uint8_t* s, int left, int hp) {
+    if (HPL == 1 && hp == 1) {
+      if (left >= kTile) tile<1, true>(s, left);
+      else tile<1, false>(s, left);
+    } else if (HPL == 1 && hp == 2) {
+      if (left >= kTile) tile<2, true>(s, left);
+      else tile<2, false>(s, left);
+    } else {
+      if (left >= kTile) tile<4, true>(s, left);
+      else tile<4, false>(s, left);
+    }
+  }
+
+  // The unit's outputs (whole), or this warp's part of them: sums [heads][DH] to po, (max, sum) [heads] to pml.
+  __device__ __forceinline__ void finish(const AttnArgs& a, int b, int g, int hp, bool whole, float* po, float2* pml) {
     const int H = heads_of_group(a, g);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -714,15 +729,49 @@ struct Warp {
           for (int i = 0; i < DH / 32; ++i)
             *reinterpret_cast<uint2*>(d + 32 * i) = make_uint2(pack_bf16x2(o[4 * i], o[4 * i + 1]), pack_bf16x2(o[4 * i + 2], o[4 * i + 3]));
         } else {
-          float* d = a.part_o + (slot * a.H + h) * DH + 4 * lr;
+          float* d = po + h * DH + 4 * lr;
 #pragma unroll
           for (int i = 0; i < DH / 32; ++i)
             *reinterpret_cast<float4*>(d + 32 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          if (lr == 0) a.part_ml[slot * a.H + h] = make_float2(m[nb][j], ls);
+          if (lr == 0) pml[h] = make_float2(m[nb][j], ls);
         }
       }
   }
 };
+
+// Columns per head set (HPL = 1): 1, 2 or 4 >= the group's heads.
+template <int HPL>
+__device__ __forceinline__ int columns(int H) {
+  return HPL == 2 || H > 2 ? 4 : H;
+}
+
+// Loads a lane's pieces of one tile, `left` keys from the rows at pk, pv, pm
+// on, into the ring's place at d.
+template <int DH>
+__device__ __forceinline__ void load_tile(const AttnArgs& a, uint32_t d, const uint8_t* pk, const uint8_t* pv,
+                                          const uint8_t* pm, int left, int lane) {
+  using S = AttnShape<DH>;
+  constexpr int CP = kTile * S::ROW / 512;  // 16-byte pieces of K (or V) per lane
+  d += lane * 16;
+  if (left >= kTile) {
+#pragma unroll
+    for (int j = 0; j < CP; ++j) cp_async_16(d + 512 * j, pk + 512 * j, 16);
+    cp_async_16(d + 2 * kTile * S::ROW, pm, 16);
+#pragma unroll
+    for (int j = 0; j < CP; ++j) cp_async_16(d + kTile * S::ROW + 512 * j, pv + 512 * j, 16);
+  } else {
+    // The sequence's last tile: what lies behind it (and perhaps behind the
+    // buffer) is not read, its place is filled with zeros.
+#pragma unroll
+    for (int j = 0; j < CP; ++j) {
+      const bool on = 16 * (lane + 32 * j) < left * S::ROW;
+      cp_async_16(d + 512 * j, on ? pk + 512 * j : a.c.k_codes, on ? 16 : 0);
+      cp_async_16(d + kTile * S::ROW + 512 * j, on ? pv + 512 * j : a.c.v_codes, on ? 16 : 0);
+    }
+    const bool on = 2 * lane < left;  // two keys per piece (the capacity is even)
+    cp_async_16(d + 2 * kTile * S::ROW, on ? pm : reinterpret_cast<const uint8_t*>(a.c.meta), on ? 16 : 0);
+  }
+}
 
 template <int DH, int HPL, int NB>
 __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(AttnArgs a) {
@@ -809,26 +858,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
     pm = reinterpret_cast<const uint8_t*>(a.c.meta) + row * 8 + lane * 16;
   };
   auto issue = [&](int i) {
-    constexpr int CP = kTile * S::ROW / 512;  // 16-byte pieces of K (or V) per lane
-    const uint32_t d = ring + i * S::TILE_BYTES + lane * 16;
-    if (wr.left >= kTile) {
-#pragma unroll
-      for (int j = 0; j < CP; ++j) cp_async_16(d + 512 * j, pk + 512 * j, 16);
-      cp_async_16(d + 2 * kTile * S::ROW, pm, 16);
-#pragma unroll
-      for (int j = 0; j < CP; ++j) cp_async_16(d + kTile * S::ROW + 512 * j, pv + 512 * j, 16);
-    } else {
-      // The sequence's last tile: what lies behind it (and perhaps behind the
-      // buffer) is not read, its place is filled with zeros.
-#pragma unroll
-      for (int j = 0; j < CP; ++j) {
-        const bool on = 16 * (lane + 32 * j) < wr.left * S::ROW;
-        cp_async_16(d + 512 * j, on ? pk + 512 * j : a.c.k_codes, on ? 16 : 0);
-        cp_async_16(d + kTile * S::ROW + 512 * j, on ? pv + 512 * j : a.c.v_codes, on ? 16 : 0);
-      }
-      const bool on = 2 * lane < wr.left;  // two keys per piece (the capacity is even)
-      cp_async_16(d + 2 * kTile * S::ROW, on ? pm : reinterpret_cast<const uint8_t*>(a.c.meta), on ? 16 : 0);
-    }
+    load_tile<DH>(a, ring + i * S::TILE_BYTES, pk, pv, pm, wr.left, lane);
     pk += kTile * S::ROW;
     pv += kTile * S::ROW;
     pm += kTile * 8;
@@ -848,12 +878,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
   w.lr = lane >> 2;
   w.lc = lane & 3;
   asm volatile("mov.b32 %0, 0x41804180;" : "=r"(w.k16));
-  // Columns per head set (HPL = 1): 1, 2 or 4 >= the group's heads.
-  auto columns = [&](int g) {
-    const int H = heads_of_group(a, g);
-    return HPL == 2 || H > 2 ? 4 : H;
-  };
-  int hp = columns(rd.g);
+  int hp = columns<HPL>(heads_of_group(a, rd.g));
   w.start(a, rd.b, rd.g, hp);
   int stage = 0;
   for (int i = 0; i < count; ++i) {
@@ -861,30 +886,131 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
     __syncwarp();
     const uint8_t* s = sm + warp * S::RING + stage * S::TILE_BYTES;
     const int left = rd.left;
-    if (HPL == 1 && hp == 1) {
-      if (left >= kTile) w.template tile<1, true>(s, left);
-      else w.template tile<1, false>(s, left);
-    } else if (HPL == 1 && hp == 2) {
-      if (left >= kTile) w.template tile<2, true>(s, left);
-      else w.template tile<2, false>(s, left);
-    } else {
-      if (left >= kTile) w.template tile<4, true>(s, left);
-      else w.template tile<4, false>(s, left);
-    }
+    w.any_tile(s, left, hp);
     __syncwarp();
     if (i + kStages < count) issue(stage);
     cp_async_commit();
     stage = stage + 1 == kStages ? 0 : stage + 1;
     rd.left = left - kTile;
     if (rd.left <= 0 || i + 1 == count) {
-      w.finish(a, rd.b, rd.g, hp, first_whole && rd.left <= 0, gw + static_cast<long long>(rd.b) * a.G + rd.g);
+      const long long slot = (gw + static_cast<long long>(rd.b) * a.G + rd.g) * a.H;
+      w.finish(a, rd.b, rd.g, hp, first_whole && rd.left <= 0, a.part_o + slot * DH, a.part_ml + slot);
       if (i + 1 == count) break;
       rd.next_unit(a);
       first_whole = true;
-      hp = columns(rd.g);
+      hp = columns<HPL>(heads_of_group(a, rd.g));
       w.start(a, rd.b, rd.g, hp);
     }
   }
+}
+
+// The same for few units of moderate length, where launches and latencies
+// count: the sequences' units take `ctas` CTAs each (a cluster), every one's
+// tiles in equal shares over its warps, and the parts are joined out of shared
+// memory: no second launch, no sums over the batch's lengths first.
+// 1 x 2048 keys, 8 groups: 4.3 us on the device (equal shares of everything and
+// a join 8.6), 4 x 4096 6.5 (10.0), 16 x 2048 8.1 (12.9).
+constexpr int kUnitCtas = 8;   // of a cluster, at most
+constexpr int kUnitTiles = 8;  // per warp, at most (see attention())
+template <int DH, int HPL, int NB>
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_unit_kernel(AttnArgs a) {
+  using S = AttnShape<DH>;
+  constexpr int MAXH = HPL * NB * 4 > 4 ? NB * 8 : 4;  // heads of a group
+  static_assert(MAXH * (DH * 4 + 8) <= S::RING, "a warp's part lies in its ring");
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ float2 joined[MAXH];  // this CTA's (max, sum)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.ctas, u = blockIdx.x / C, rank = blockIdx.x - u * C, b = u / a.G, g = u - b * a.G;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = keys_of(a, b), tiles = tiles_of(n), H = heads_of_group(a, g);
+  if (n == 0) {  // zeros
+    if (rank == 0)
+      for (int i = tid; i < H * (DH / 8); i += kAttnThreads)
+        reinterpret_cast<uint4*>(out_row(a, b, g, i / (DH / 8), DH))[i % (DH / 8)] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const int share = (tiles + C * kAttnWarps - 1) / (C * kAttnWarps);
+  const int first = (warp * C + rank) * share, count = min(share, tiles - first);
+  uint8_t* mine = sm + warp * S::RING;
+  if (count > 0) {
+    const long long row = (static_cast<long long>(b) * a.G + g) * a.c.capacity + static_cast<long long>(first) * kTile;
+    const uint8_t* pk = a.c.k_codes + row * S::ROW + lane * 16;
+    const uint8_t* pv = a.c.v_codes + row * S::ROW + lane * 16;
+    const uint8_t* pm = reinterpret_cast<const uint8_t*>(a.c.meta) + row * 8 + lane * 16;
+    const int left = n - first * kTile;
+    auto issue = [&](int i) {
+      if (i < count)
+        load_tile<DH>(a, smem_u32(mine) + i % kStages * S::TILE_BYTES, pk + static_cast<long long>(i) * kTile * S::ROW,
+                      pv + static_cast<long long>(i) * kTile * S::ROW, pm + static_cast<long long>(i) * kTile * 8, left - i * kTile, lane);
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) issue(i);
+    Warp<DH, HPL, NB> w;
+    w.lr = lane >> 2;
+    w.lc = lane & 3;
+    asm volatile("mov.b32 %0, 0x41804180;" : "=r"(w.k16));
+    const int hp = columns<HPL>(H);
+    w.start(a, b, g, hp);
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      w.any_tile(mine + i % kStages * S::TILE_BYTES, left - i * kTile, hp);
+      __syncwarp();
+      issue(i + kStages);
+    }
+    float* po = reinterpret_cast<float*>(mine);
+    w.finish(a, b, g, hp, tiles == 1, po, reinterpret_cast<float2*>(po + MAXH * DH));
+  }
+  if (tiles == 1) return;  // the whole cluster
+  // This CTA's warps (those with tiles come first), into warp 0's place.
+  __syncthreads();
+  const int have = min(kAttnWarps, ((tiles + share - 1) / share - rank + C - 1) / C);  // <= 0: none
+  auto part_o = [&](int w) { return reinterpret_cast<float*>(sm + w * S::RING); };
+  auto part_ml = [&](int w) { return reinterpret_cast<const float2*>(part_o(w) + MAXH * DH); };
+  if (have > 0)
+    for (int e = tid; e < H * DH; e += kAttnThreads) {
+      const int h = e / DH;
+      float m = -INFINITY, l = 0.0f, o = 0.0f;
+      for (int w = 0; w < have; ++w) m = fmaxf(m, part_ml(w)[h].x);
+      const float mu = m == -INFINITY ? 0.0f : m;
+      for (int w = 0; w < have; ++w) {
+        const float2 v = part_ml(w)[h];
+        const float f = exp2_ftz(v.x - mu);
+        l = fmaf(f, v.y, l);
+        o = fmaf(f, part_o(w)[e], o);
+      }
+      part_o(0)[e] = o;
+      if (e % DH == 0) joined[h] = make_float2(m, l);
+    }
+  const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  cluster.sync();
+  const int ctas = min(C, (tiles + share - 1) / share);  // those with tiles: the first ones
+  for (int e = rank * kAttnThreads + tid; e < H * DH; e += C * kAttnThreads) {
+    const int h = e / DH;
+    float2 ml[kUnitCtas];
+    float x[kUnitCtas], m = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kUnitCtas; ++r) {
+      ml[r] = make_float2(-INFINITY, 0.0f);
+      x[r] = 0.0f;
+      if (r < ctas) {
+        ml[r] = cluster.map_shared_rank(joined, r)[h];
+        x[r] = cluster.map_shared_rank(part_o(0), r)[e];
+        m = fmaxf(m, ml[r].x);
+      }
+    }
+    const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int r = 0; r < kUnitCtas; ++r) {
+      const float f = exp2_ftz(ml[r].x - mu);
+      l = fmaf(f, ml[r].y, l);
+      o = fmaf(f, x[r], o);
+    }
+    out_row(a, b, g, h, DH)[e - h * DH] = __bfloat16_as_ushort(__float2bfloat16_rn(o / l));
+  }
+  cluster.sync();  // the others' memory stays until it is read
 }
 
 // Joins the parts of the units that lie in several shares: one CTA per unit
@@ -952,8 +1078,40 @@ int launch_attn(const AttnArgs& a, void* stream) {
                     AttnShape<DH>::smem(), stream, a);
 }
 
+template <int DH, int HPL, int NB>
+int launch_unit(AttnArgs a, int ctas, void* stream) {
+  a.ctas = ctas;
+  const int e = ensure_smem<kv4_attn_unit_kernel<DH, HPL, NB>>(static_cast<int>(AttnShape<DH>::smem()));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.G * ctas);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = AttnShape<DH>::smem();
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kv4_attn_unit_kernel<DH, HPL, NB>, a));
+}
+
 template <int DH>
 int attention(const AttnArgs& a, void* stream) {
+  // A cluster per unit as long as all are resident (256: clusters do not fill
+  // the SMs' last places; 72 units with 4 CTAs each took two rounds) and a
+  // warp has at most 8 tiles. 16 x 8192 keys of 8 groups, in us: equal lengths
+  // 28 against 34 for equal shares, lengths spread evenly 27 (28), one long
+  // sequence among short ones 18 (18). 2 x 32768: 17.2 (16.8).
+  const long long all = static_cast<long long>(a.B) * a.G;
+  int ctas = kUnitCtas;
+  while (ctas > 1 && all * ctas > 256) ctas /= 2;
+  if (all <= 148 * kAttnCtasPerSm && a.T <= ctas * kAttnWarps * kTile * kUnitTiles)
+    return a.H <= 4 ? launch_unit<DH, 1, 1>(a, ctas, stream)
+           : a.H <= 8 ? launch_unit<DH, 2, 1>(a, ctas, stream)
+                      : launch_unit<DH, 2, 2>(a, ctas, stream);
   const int e = a.H <= 4 ? launch_attn<DH, 1, 1>(a, stream)
                 : a.H <= 8 ? launch_attn<DH, 2, 1>(a, stream)
                            : launch_attn<DH, 2, 2>(a, stream);

@@ -179,6 +179,20 @@ ATTN = {
     "many_sequences": (150, 8, 1, True, 64, 70, None),
     "wide_batch": (700, 2, 1, True, 32, 200, [(37 * b) % 201 if b % 3 else 0 for b in range(700)]),
     "one_live_sequence": (300, 1, 2, False, 64, 3000, [0] * 299 + [3000]),
+    # A cluster of 8, 4, 2 and 1 CTAs per (sequence, group), then equal shares with a join.
+    "unit_8_tiles_per_warp": (2, 1, 1, True, 64, 32768, [32768, 32000]),
+    "units_60": (20, 3, 2, True, 64, 1500, [(311 * b) % 1501 for b in range(20)]),
+    "units_100": (25, 4, 4, False, 32, 1500, [(311 * b) % 1501 for b in range(25)]),
+    "units_200_heads_6": (25, 8, 5, True, 64, 900, [(201 * b) % 901 for b in range(25)]),
+    "units_296": (37, 8, 1, True, 64, 4096, [(1009 * b) % 4097 for b in range(37)]),
+    "units_297": (297, 1, 4, False, 64, 1000, None),
+    "long_k1": (1, 2, 1, True, 64, 40000, None),
+    "long_dense4": (2, 1, 4, False, 64, 33001, [33001, 4095]),
+    "long_dh32_k2": (2, 1, 2, True, 32, 33001, [17, 33001]),
+    "long_heads_8": (1, 1, 8, False, 64, 33001, None),
+    "long_heads_9": (1, 2, 8, True, 64, 33001, None),
+    "long_heads_16": (1, 1, 16, False, 64, 33001, None),
+    "long_heads_16_dh32": (1, 1, 15, True, 32, 33001, None),
     "nothing_live": (5, 2, 1, True, 64, 50, [0, -1, 0, -7, 0]),
 }
 
