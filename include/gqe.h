@@ -536,7 +536,7 @@ gqe_status gqe_kv4_read(const gqe_config* cfg, const gqe_kv4* cache, const int32
  * 0). lens [B] int32, clamped to 0..cfg->T (NULL: cfg->T <= capacity; cfg->T
  * sizes the launch, so a bound near the longest sequence is best). A sequence
  * without keys gets zeros. Sums are fp32 and divided at the end: 32 keys |V|
- * has to stay below 2^127.
+ * has to stay below 2^127; so do the scores, q of any finite size.
  * Q [B, G, k, d_head] (dense heads: cfg->k = M); Qs [B, d_head] or NULL;
  * out [B, ldo], ldo a multiple of 8: head (g, s) at column (g*k + s)*d_head,
  * the shared head at k*G*d_head. At most 16 heads per group, B*G <= 65535.

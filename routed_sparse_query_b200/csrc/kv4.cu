@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    undone in q. Of a row's 32-bit word that is one shift and four ANDs for
 //    eight elements. q goes in as q 2^(14 - e), e the exponent of the head's
 //    largest element: exact but for elements 2^-38 of that. Then
-//    s = scale_k sum(q n) + zero_k sum(q) in fp32.
+//    s = scale_k sum(q n) + zero_k sum(q) in fp32, in units of 2^10 (kUnit).
 //  - Output, dims x heads, over the keys: with n in the upper four mantissa
 //    bits, 0x4180 | n << 3 is the bf16 16 + n. The weight operand is p scale_v
 //    in bf16 (fp16 would not hold the range of the scales); 24 times the sum of
@@ -328,6 +328,10 @@ constexpr int kTile = 64;   // keys per tile
 constexpr int kStages = 3;  // tiles in flight per warp
 constexpr int kAttnCtasPerSm = 2;
 constexpr int kMaxAttnWarps = 148 * kAttnCtasPerSm * kAttnWarps;
+// Scores and their maxima are kept in units of 2^10: the factor of a query near
+// bf16's largest, and the sum of its elements, then stay within fp32. The
+// exponential's difference undoes it in the multiply-add that it is.
+constexpr float kUnit = 1024.0f;
 
 struct AttnArgs {
   const uint16_t* Q;   // [B][G][k][dh]
@@ -339,7 +343,7 @@ struct AttnArgs {
   // Part of warp w and unit u = b G + g: slot w + u (along the shares, w + u
   // grows with every part, and a unit's parts are consecutive).
   float* part_o;       // [slots][H][dh]
-  float2* part_ml;     // [slots][H]: max, sum
+  float2* part_ml;     // [slots][H]: max (in kUnit), sum
   long long* starts;   // [B + 1]: tiles before sequence b; then the share
   uint16_t* out;
   int ldo;
@@ -410,6 +414,8 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+// 2^(a - b) of two maxima in kUnit; nothing but -inf so far (b as 0): 0.
+__device__ __forceinline__ float exp2_less(float a, float b) { return exp2_ftz(fmaf(a, kUnit, -b * kUnit)); }
 
 // Four 8 x 8 blocks of 16-bit elements, each read by rows (lane 8 i + j: row j
 // of block i) and handed out by columns: lane (lr, lc) gets elements 2 lc and
@@ -486,7 +492,7 @@ struct Warp {
 #pragma unroll
       for (int i = 0; i < DH / 4; ++i) {
         mx = fmaxf(mx, fabsf(v[i]));
-        sum += v[i];
+        sum = fmaf(v[i], 1.0f / kUnit, sum);  // exact terms: bf16's least times 2^-10 is an fp32
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
@@ -506,7 +512,7 @@ struct Warp {
         qf[nb][s][1] = *reinterpret_cast<const uint32_t*>(&hi);
       }
       // Score columns 2 lc (and 2 lc + 1): their factors from the lanes that formed them.
-      const float f = a.scale_log2 * pow2(e) * 1024.0f;  // 2^(24 - 14 + e)
+      const float f = a.scale_log2 * pow2(e);  // 2^(24 - 14 + e), in kUnit
 #pragma unroll
       for (int j = 0; j < HPL; ++j) {
         fac[nb][j] = __shfl_sync(0xffffffffu, f, (2 * lc + j) * 4);
@@ -595,9 +601,9 @@ struct Warp {
         for (int o = HP; o < 32; o <<= 1) mt[nb][j] = fmaxf(mt[nb][j], __shfl_xor_sync(0xffffffffu, mt[nb][j], o));
         const float mn = fmaxf(m[nb][j], mt[nb][j]);
         grown = grown || mn > m[nb][j];
-        al[nb][j] = m[nb][j] == mn ? 1.0f : exp2_ftz(m[nb][j] - mn);
+        al[nb][j] = m[nb][j] == mn ? 1.0f : exp2_less(m[nb][j], mn);
         m[nb][j] = mn;
-        mt[nb][j] = mn == -INFINITY ? 0.0f : mn;  // nothing but -inf so far: weights 0
+        mt[nb][j] = mn == -INFINITY ? 0.0f : mn * kUnit;  // nothing but -inf so far: weights 0
       }
     if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -626,7 +632,7 @@ struct Warp {
           float w2[2] = {0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < HPL; ++j) {
-            const float p = exp2_ftz(ps[nb][j][i][r] - mt[nb][j]);
+            const float p = exp2_ftz(fmaf(ps[nb][j][i][r], kUnit, -mt[nb][j]));
             l[nb][j] += p;
             zs[nb][j] = fmaf(p, vc, zs[nb][j]);
             w2[j] = p * vs;
@@ -918,7 +924,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_unit_ke
   constexpr int MAXH = HPL * NB * 4 > 4 ? NB * 8 : 4;  // heads of a group
   static_assert(MAXH * (DH * 4 + 8) <= S::RING, "a warp's part lies in its ring");
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ float2 joined[MAXH];  // this CTA's (max, sum)
+  __shared__ float2 joined[MAXH];  // this CTA's (max in kUnit, sum)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.ctas, u = blockIdx.x / C, rank = blockIdx.x - u * C, b = u / a.G, g = u - b * a.G;
   pdl_wait();
@@ -977,7 +983,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_unit_ke
       const float mu = m == -INFINITY ? 0.0f : m;
       for (int w = 0; w < have; ++w) {
         const float2 v = part_ml(w)[h];
-        const float f = exp2_ftz(v.x - mu);
+        const float f = exp2_less(v.x, mu);
         l = fmaf(f, v.y, l);
         o = fmaf(f, part_o(w)[e], o);
       }
@@ -1004,7 +1010,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_unit_ke
     const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int r = 0; r < kUnitCtas; ++r) {
-      const float f = exp2_ftz(ml[r].x - mu);
+      const float f = exp2_less(ml[r].x, mu);
       l = fmaf(f, ml[r].y, l);
       o = fmaf(f, x[r], o);
     }
@@ -1040,7 +1046,7 @@ __global__ void __launch_bounds__(kJoinRows * DH) kv4_join_kernel(AttnArgs a) {
 #pragma unroll 4
   for (int c = row; c < parts; c += rows) {
     const float2 v = ml[static_cast<long long>(c) * a.H];
-    const float w = exp2_ftz(v.x - mu);
+    const float w = exp2_less(v.x, mu);
     l = fmaf(w, v.y, l);
     o = fmaf(w, po[static_cast<long long>(c) * a.H * DH], o);
   }
@@ -1055,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinRows * DH) kv4_join_kernel(AttnArgs a) {
   const float all = m == -INFINITY ? 0.0f : m;
   o = l = 0.0f;
   for (int r = 0; r < rows; ++r) {
-    const float w = exp2_ftz(jm[r] - all);
+    const float w = exp2_less(jm[r], all);
     l = fmaf(w, jl[r], l);
     o = fmaf(w, jo[r * DH + d], o);
   }
