@@ -292,14 +292,18 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    s = scale_k sum(q n) + zero_k sum(q) in fp32, in units of 2^10 (kUnit).
 //  - Output, dims x heads, over the keys: with n in the upper four mantissa
 //    bits, 0x4180 | n << 3 is the bf16 16 + n. The weight operand is p scale_v
-//    in bf16 (fp16 would not hold the range of the scales); 24 times the sum of
-//    the same rounded weights is taken off again, which leaves sum p scale_v
-//    (n - 8), and the rest, sum p (zero_v + 8 scale_v), is kept in fp32. The
-//    rounding of p thus meets codes around zero, |n - 8| <= 8. The tensor cores
-//    cut their sums off where they would round, always downwards: each tile's
-//    sums start from zero and join the running ones in fp32 (carried on in the
-//    accumulator, and with 128 + n, the 64 x 32k outputs were 1.3 % off).
-//  - Up to 4 heads per group: the heads sit in the even columns, 4 / HP times
+//    in two bf16 parts (fp16 would not hold the range of the scales; one part
+//    alone, 8 bits, put the outputs 0.1 to 0.15 % off beside their own rounding's
+//    0.17 %; the second costs 1 % at 64 x 32k, 15 % with 8 heads, 20 % with
+//    16): together 2^-16 of it, against codes taken around zero, since 24
+//    times the sum of the same parts is taken off again, which leaves
+//    sum p scale_v (n - 8); the rest, sum p (zero_v + 8 scale_v), is kept in
+//    fp32. The tensor cores cut their sums off where they would round, always
+//    downwards: each tile's sums start from zero and join the running ones in
+//    fp32 (carried on in the accumulator, and with 128 + n, the 64 x 32k outputs
+//    were 1.3 % off).
+//  - Up to 4 heads per group: the heads sit in the even columns (the second
+//    part of a weight in the odd one beside it: no product more), 4 / HP times
 //    over (HP = 1, 2 or 4 >= the group's heads), so the scores' accumulator
 //    holds one head per lane and every copy of the column can take other keys:
 //    lane column lc forms the weights of head lc % HP for the 16-key blocks
@@ -620,8 +624,13 @@ struct Warp {
           }
         }
     }
-    // Weights p scale_v of this lane's blocks, packed as (column 2 lc, 2 lc + 1).
-    uint32_t pk[NB][OWN][2];
+    // Weights p scale_v of this lane's blocks, in two bf16 parts: the upper half
+    // of the fp32 value, and what that leaves. pk[0]: column 2 lc in the low half,
+    // 2 lc + 1 in the high half. One head per lane: the first part in column
+    // 2 lc, the second beside it in 2 lc + 1, the same products for both; two
+    // heads: the second parts in pk[1], products of their own.
+    constexpr int PARTS = HPL;
+    uint32_t pk[PARTS][NB][OWN][2];
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
 #pragma unroll
@@ -629,29 +638,40 @@ struct Warp {
         const float vs = bf16_f(mv[i][r] & 0xffffu), vc = fmaf(8.0f, vs, __uint_as_float(mv[i][r] & 0xffff0000u));
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float w2[2] = {0.0f, 0.0f};
+          float hi[HPL], rest[HPL];
 #pragma unroll
           for (int j = 0; j < HPL; ++j) {
             const float p = exp2_ftz(fmaf(ps[nb][j][i][r], kUnit, -mt[nb][j]));
             l[nb][j] += p;
             zs[nb][j] = fmaf(p, vc, zs[nb][j]);
-            w2[j] = p * vs;
+            const float w = p * vs;
+            hi[j] = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+            rest[j] = w - hi[j];
           }
-          const uint32_t w = pack_bf16x2(w2[0], w2[1]);
-          pk[nb][i][r] = w;
+          uint32_t second;
+          if constexpr (HPL == 1) {
+            second = pk[0][nb][i][r] = pack_bf16x2(hi[0], rest[0]);
+          } else {
+            pk[0][nb][i][r] = __byte_perm(__float_as_uint(hi[0]), __float_as_uint(hi[HPL - 1]), 0x7632);
+            second = pk[PARTS - 1][nb][i][r] = pack_bf16x2(rest[0], rest[HPL - 1]);
+          }
 #pragma unroll
-          for (int j = 0; j < HPL; ++j)  // the weights as rounded, of the codes' 16 + 8
-            zs[nb][j] = fmaf(-24.0f, __uint_as_float(j == 0 ? w << 16 : w & 0xffff0000u), zs[nb][j]);
+          for (int j = 0; j < HPL; ++j) {  // the weights as they go in, of the codes' 16 + 8
+            const float lo = __uint_as_float(HPL == 1 || j == 1 ? second & 0xffff0000u : second << 16);
+            zs[nb][j] = fmaf(-24.0f, hi[j], fmaf(-24.0f, lo, zs[nb][j]));
+          }
         }
       }
     float sum[NB][MT][4];  // of this tile
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      uint32_t pw[NB][2];
+      uint32_t pw[PARTS][NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int c = 0; c < PARTS; ++c)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) pw[nb][r] = transpose8(R == 1 || part == u % R ? pk[nb][u / R][r] : 0u);
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) pw[c][nb][r] = transpose8(R == 1 || part == u % R ? pk[c][nb][u / R][r] : 0u);
       // V: 16-bit column lr (4 codes) of keys 2 lc, 2 lc + 1 (+ 8), for each
       // 32 elements of a row: element 32 x + 4 lr + nibble.
       uint32_t x[2 * (DH / 32)];  // [32 elements][keys + 8 r]
@@ -667,8 +687,9 @@ struct Warp {
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          if (u == 0) mma_bf16_first(sum[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
-          else mma_bf16(sum[nb][t], f[0], f[1], f[2], f[3], pw[nb][0], pw[nb][1]);
+          if (u == 0) mma_bf16_first(sum[nb][t], f[0], f[1], f[2], f[3], pw[0][nb][0], pw[0][nb][1]);
+          else mma_bf16(sum[nb][t], f[0], f[1], f[2], f[3], pw[0][nb][0], pw[0][nb][1]);
+          if (PARTS == 2) mma_bf16(sum[nb][t], f[0], f[1], f[2], f[3], pw[PARTS - 1][nb][0], pw[PARTS - 1][nb][1]);
         }
       }
     }
@@ -678,8 +699,8 @@ struct Warp {
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int j = 0; j < HPL; ++j) {
-          acc[nb][t][j] += sum[nb][t][j];
-          acc[nb][t][j + HPL] += sum[nb][t][j + 2];
+          acc[nb][t][j] += HPL == 1 ? sum[nb][t][0] + sum[nb][t][1] : sum[nb][t][j];
+          acc[nb][t][j + HPL] += HPL == 1 ? sum[nb][t][2] + sum[nb][t][3] : sum[nb][t][j + 2];
         }
   }
 
