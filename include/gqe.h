@@ -412,7 +412,9 @@ gqe_status gqe_layer_bwd(const gqe_config* cfg, const gqe_bf16* x, const float* 
  *     angle = pos[axis[i]][row] * inv_freq[i]
  *     (a, b) <- scale * (a cos - b sin, a sin + b cos)
  *   elements d_rot and up pass.
- * Angles are formed in fp64, the rest in fp32, one rounding at the end.
+ * Angles are formed in fp64, the rest in fp32, one rounding at the end: with
+ * the norm |x| has to stay below 2^60 (its square's sum in fp32's range) and,
+ * if eps = 0, a row's largest above 2^-60.
  */
 #define GQE_ROPE_NORM 1u     /* norm each row over d_head first */
 #define GQE_ROPE_ADJACENT 2u /* pairs of adjacent elements */
