@@ -10,8 +10,9 @@
 // wherever it is computed. A row with an infinity or NaN gets scale = zero =
 // NaN: all of it reads as NaN.
 //
-// Storing 4 x 8192 tokens of 8 groups (86 MB): 26 us, bound by the arithmetic
-// (ALU 54 % busy); reading them back: 15 us (5.8 TB/s).
+// Storing 4 x 8192 tokens of 8 groups (86 MB): 26 us, bound by latency as much as
+// by arithmetic: at 78 registers 32 % of the warps are resident, ALU 49 % and DRAM
+// 28 % busy, 2.5 instructions per cycle. Reading them back: 15 us (5.8 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 // Decode attention: o = softmax(q . K / sqrt(dh)) V over the sequence's keys.
 //
 // Bytes: d_head + 8 per key and KV group (codes of K and V, two (scale, zero)
-// pairs), a quarter of the bf16 cache's 4 d_head. At that rate the CUDA cores
+// pairs), 28 % of the bf16 cache's 4 d_head (31 % at 32). At that rate the CUDA cores
 // would bound the kernel (two products and two conversions per element and
 // head), so the products run on the tensor cores (mma.sync m16n8k16: with at
 // most 16 query rows a 128-row tcgen05 tile would be nine tenths padding)
@@ -294,8 +295,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 //    bits, 0x4180 | n << 3 is the bf16 16 + n. The weight operand is p scale_v
 //    in two bf16 parts (fp16 would not hold the range of the scales; one part
 //    alone, 8 bits, put the outputs 0.1 to 0.15 % off beside their own rounding's
-//    0.17 %; the second costs 1 % at 64 x 32k, 15 % with 8 heads, 20 % with
-//    16): together 2^-16 of it, against codes taken around zero, since 24
+//    0.17 %; the second costs 1 to 3 % up to 4 heads, about 15 % with 8 and 20 %
+//    with 16): together 2^-16 of it, against codes taken around zero, since 24
 //    times the sum of the same parts is taken off again, which leaves
 //    sum p scale_v (n - 8); the rest, sum p (zero_v + 8 scale_v), is kept in
 //    fp32. The tensor cores cut their sums off where they would round, always
@@ -322,10 +323,12 @@ __global__ void __launch_bounds__(kThreads) read_kernel(StoreArgs a) {
 // nine 512-byte pieces). A unit that lies in one warp's share is written out
 // by it; the parts of the others are joined by a second kernel.
 //
-// Measured: 64 x 32768 keys, 8 groups, one or two heads each: 227 us (1.21 GB,
-// 82 % of the copy rate, the SMs at 1.62 GHz under the power cap; 203 us in a
-// short run); 192 x 32768: 97 % of the copy rate; ALU pipe 60 % and tensor pipe
-// 30 % busy. 1 x 2048 keys: 7.5 us, one launch (kv4_attn_unit_kernel).
+// Measured: 64 x 32768 keys, 8 groups, one or two heads each: 235 us (1.21 GB,
+// 80 % of the copy rate, under the power cap; 201 us in a short run); 192 x 32768
+// in a short run: 90 to 98 % of the copy rate; ALU pipe 59 % and tensor pipe 30 %
+// busy. 1 x 2048 keys: 7.4 us, one launch (kv4_attn_unit_kernel). 9 to 16 heads
+// (the registers of two column blocks pass 128, 0.7 KB of them spill): 32 x 32768
+// keys of 4 groups with 16 heads each 149 to 160 us, floor 47.
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kTile = 64;   // keys per tile
@@ -941,8 +944,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm) kv4_attn_kernel(
 // count: the sequences' units take `ctas` CTAs each (a cluster), every one's
 // tiles in equal shares over its warps, and the parts are joined out of shared
 // memory: no second launch, no sums over the batch's lengths first.
-// 1 x 2048 keys, 8 groups: 4.3 us on the device (equal shares of everything and
-// a join 8.6), 4 x 4096 6.5 (10.0), 16 x 2048 8.1 (12.9).
+// 1 x 2048 keys, 8 groups: 4.1 us on the device, 4 x 4096 6.2, 16 x 2048 9.8 (8.1
+// from L2); equal shares of everything and a join took 8.6, 10.0 and 12.9.
 constexpr int kUnitCtas = 8;   // of a cluster, at most
 constexpr int kUnitTiles = 8;  // per warp, at most (see attention())
 template <int DH, int HPL, int NB>

@@ -22,7 +22,12 @@
 // Measured, 8 groups of d_head 64, share of the copy rate: forward of 4 x 8192
 // tokens 29 us (142 MB, 76 %), of 262144 tokens 202 us (1.14 GB, 87 %; 181 us
 // in a short run with one axis); backward of 4 x 8192 tokens and 25 heads
-// 91 us (524 MB, 89 %). 64 tokens: 7 us, the launch.
+// 91 us (524 MB, 89 %). 64 tokens: 7 us, the launch. Backward of 2048 tokens
+// (floor 3.4 us): 12 us, 10 of them on the device: a thread's rows one after the
+// other, the first behind the angles, then the kernel of the weights' gradients.
+// In the layer's backward (gradients in parts, the general form): 2048 tokens 19
+// us cold; with the forward's rotation 21 of 362 us, at 4 x 8192 tokens of the
+// pool 171 of 8470.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
