@@ -1,12 +1,15 @@
 """The router's balance loss (gqe_balance_stats, gqe_balance_loss) against the
 fp64 definition.
 
-Tolerances. Counts are equal. p and lse come from fp32 expf, a sum of M <= 64
-terms and a division: at most 2^-17 relative (64 * 2^-24 = 2^-18 for the sum, a
-few 2^-24 for the rest), lse 2^-17 of 1 + |lse|. sums: those errors plus at most
-2^-18 for the fp32 partial sums. dz: 2^-15 of the terms' sizes -- with the loads
-taken around their mean 1/M, as cancellation would have cost more than that near
-balance."""
+Tolerances. Counts are equal. p and lse come from the hardware's exponential to
+base 2, reciprocal and logarithm and a sum of M <= 64 terms: at most 2^-17
+relative (64 * 2^-24 = 2^-18 for the sum; the exponential's argument, a difference
+of up to 18 times log2 e, two roundings of 2^-24 of 26 and the constant's 2^-26: 2^-18.6
+of the term; 2^-22 each for the three functions; together 2^-17.1), lse 2^-17 of
+1 + |lse|. sums: those errors plus at most 2^-18 for the fp32 partial sums (of a
+thread, a CTA, and the CTAs that one thread of the last step takes). dz: 2^-15 of
+the terms' sizes -- with the loads taken around their mean 1/M, as cancellation
+would have cost more than that near balance."""
 import numpy as np
 import pytest
 import torch

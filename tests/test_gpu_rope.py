@@ -2,12 +2,13 @@
 the fp64 definition.
 
 Tolerances. Forward: one rounding to bf16 (2^-8 of the value) on fp32 arithmetic
-whose error is at most 2^-18 of |a| + |b| of the rotated pair: the angle reaches
-fp32 as a fraction of a turn (2^-25 turns = 2^-22.3 rad), sincospi, rsqrt and the
-products add a few 2^-24 each, and the mean of d_head squares at most 2^-18 / 2 of
-rstd. Backward (fp32 out): the same relative error on the terms of
-dx = rstd (gw - xh mean(gw xh)); the row's sums of up to 64 terms add 64 * 2^-24 =
-2^-18 of their absolute sum; 2^-16 of the terms' sizes covers both. Weight
+whose error is at most 2^-18 of |a| + |b| of the rotated pair: the mean of d_head
+squares at most 2^-18 / 2 = 2^-19 of rstd; the hardware's sine and cosine within
+half a turn 2^-21.2 (their stated largest error, absolute); the angle, which
+reaches fp32 as a fraction of a turn, 2^-25 turns = 2^-22.3 rad; rsqrt and the
+products a few 2^-24: together 2^-18.5. Backward (fp32 out): the same relative
+error on the terms of dx = rstd (gw - xh mean(gw xh)); the row's sums of up to 64
+terms add 64 * 2^-24 = 2^-18 of their absolute sum; 2^-16 of the terms' sizes covers both. Weight
 gradients: the terms' 2^-17 and at most 64 sequential fp32 additions (2^-18) at
 these sizes, of the sum of absolute terms: 2^-16."""
 import numpy as np
